@@ -1,0 +1,388 @@
+// Entry points of the packed-sequence operators: argument checks, workspace
+// layout and launches (included by prism.cu, whose helpers it uses).
+#pragma once
+
+#include "block_norm.cuh"
+#include "packed_simple.cuh"
+
+namespace prism {
+
+static bool strides_ok(const int64_t s[2]) {
+  return (s[0] == 0 && s[1] == 0) || (s[0] > 0 && s[1] > 0 && s[0] % 8 == 0 && s[1] % 8 == 0);
+}
+// Strides of a [rows, heads, D] tensor; for a written one, no two elements may coincide.
+static bool fill_strides(const int64_t in[2], int64_t rows, int heads, int D, bool written, int64_t out[2]) {
+  if (!strides_ok(in)) return false;
+  out[0] = in[0] ? in[0] : (int64_t)heads * D;
+  out[1] = in[1] ? in[1] : D;
+  if (out[0] >= ((int64_t)1 << 36) || out[1] >= ((int64_t)1 << 36)) return false;
+  if (!written) return true;
+  const bool rows_outer = (heads == 1 || out[1] >= D) && (rows <= 1 || out[0] >= (heads - 1) * out[1] + D);
+  const bool heads_outer = (rows <= 1 || out[0] >= D) && (heads == 1 || out[1] >= (rows - 1) * out[0] + D);
+  return rows_outer || heads_outer;
+}
+
+static bool even_split(int64_t rows, int seqs) { return rows % seqs == 0; }
+
+static int check_packed(const prism_packed_params *p) {
+  if (!p) return fail(PRISM_EINVAL, "packed params is NULL");
+  if (p->seqs < 1) return fail(PRISM_EINVAL, "packed: seqs must be positive");
+  if (p->heads < 1 || p->kv_heads < 1 || p->heads % p->kv_heads)
+    return fail(PRISM_EINVAL, "packed: heads must be a positive multiple of kv_heads");
+  if (p->heads / p->kv_heads > 128) return fail(PRISM_EINVAL, "packed: at most 128 query heads per kv head");
+  if (p->kv_heads > 65535) return fail(PRISM_EINVAL, "packed: at most 65535 kv heads");
+  if (p->head_dim != 64 && p->head_dim != 128) return fail(PRISM_EINVAL, "packed: head_dim must be 64 or 128");
+  if (p->q_rows < 0 || p->k_rows < 0 || p->q_rows > 0x7fffff00LL || p->k_rows > 0x7fffff00LL)
+    return fail(PRISM_EINVAL, "packed: row counts must be in [0, 2^31 - 256]");
+  if (!(p->scale >= 0.f) || std::isinf(p->scale)) return fail(PRISM_EINVAL, "packed: scale must be finite and >= 0");
+  return PRISM_OK;
+}
+
+static Offsets make_offsets(const int32_t *off, int seqs, int64_t rows) {
+  return Offsets{off, seqs, (int)(rows / seqs), (int)rows};
+}
+
+// Common part of the kernel arguments; the caller has checked p.
+static int packed_args(const prism_packed_params *p, const void *q, const void *k, const void *v, const int32_t *q_off,
+                       const int32_t *k_off, const int32_t *k_used, PackedArgs *a) {
+  if ((p->q_rows && !q) || (p->k_rows && (!k || !v))) return fail(PRISM_EINVAL, "packed: NULL tensor");
+  if (!aligned16(q) || !aligned16(k) || !aligned16(v)) return fail(PRISM_EINVAL, "packed: tensors must be 16-byte aligned");
+  if ((!q_off && !even_split(p->q_rows, p->seqs)) || (!k_off && !even_split(p->k_rows, p->seqs)))
+    return fail(PRISM_EINVAL, "packed: without offsets the rows must split evenly over the sequences");
+  if (!fill_strides(p->q_stride, p->q_rows, p->heads, p->head_dim, false, a->sq) ||
+      !fill_strides(p->k_stride, p->k_rows, p->kv_heads, p->head_dim, false, a->sk) ||
+      !fill_strides(p->v_stride, p->k_rows, p->kv_heads, p->head_dim, false, a->sv) ||
+      !fill_strides(p->o_stride, p->q_rows, p->heads, p->head_dim, true, a->so))
+    return fail(PRISM_EINVAL, "packed: strides must be positive multiples of 8, and outputs must not overlap themselves");
+  a->qs = make_offsets(q_off, p->seqs, p->q_rows);
+  a->ks = make_offsets(k_off, p->seqs, p->k_rows);
+  a->k_used = k_used;
+  a->heads = p->heads;
+  a->kv_heads = p->kv_heads;
+  a->group = p->heads / p->kv_heads;
+  a->causal = p->causal != 0;
+  a->scale = p->scale > 0.f ? p->scale : 1.f / std::sqrt((float)p->head_dim);
+  a->scale_log2 = a->scale * kLog2e;
+  a->q = static_cast<const __nv_bfloat16 *>(q);
+  a->k = static_cast<const __nv_bfloat16 *>(k);
+  a->v = static_cast<const __nv_bfloat16 *>(v);
+  return PRISM_OK;
+}
+
+struct PackedBwdWs {
+  size_t delta, lse2, total;
+  explicit PackedBwdWs(const prism_packed_params *p) {
+    const size_t n = (size_t)p->q_rows * p->heads;
+    delta = 0;
+    lse2 = align256(n * 4);
+    total = lse2 + align256(n * 4);
+  }
+};
+
+template <int D>
+static int launch_packed_fwd(const prism_packed_params *p, const PackedArgs &a, cudaStream_t st) {
+  if (p->q_rows == 0) return PRISM_OK;
+  const dim3 grid((unsigned)slot_bound(p->q_rows, p->seqs, a.group, 8), a.kv_heads);
+  PRISM_TRACED("packed_fwd_simple_kernel", st, packed_fwd_simple_kernel<D><<<grid, 256, 0, st>>>(a));
+  return PRISM_OK;
+}
+
+template <int D>
+static int launch_packed_bwd(const prism_packed_params *p, const PackedArgs &a, float *delta, float *lse2,
+                             cudaStream_t st) {
+  if (p->q_rows) {
+    const int64_t threads = (int64_t)p->q_rows * p->heads * (D / 4);
+    PRISM_TRACED("packed_stats_kernel", st, packed_stats_kernel<D><<<(unsigned)((threads + 255) / 256), 256, 0, st>>>(a, a.o, delta, lse2));
+    const dim3 qgrid((unsigned)slot_bound(p->q_rows, p->seqs, a.group, 8), a.kv_heads);
+    PRISM_TRACED("packed_dq_simple_kernel", st, packed_dq_simple_kernel<D><<<qgrid, 256, 0, st>>>(a));
+  }
+  if (p->k_rows) {
+    const dim3 kgrid((unsigned)slot_bound(p->k_rows, p->seqs, 1, 8), a.kv_heads);
+    PRISM_TRACED("packed_dkdv_simple_kernel", st, packed_dkdv_simple_kernel<D><<<kgrid, 256, 0, st>>>(a));
+  }
+  return PRISM_OK;
+}
+
+// ---- block norms -----------------------------------------------------------------
+
+static bool norm_row_stride(int64_t in, int C, int64_t *out) {
+  *out = in ? in : C;
+  return in == 0 || (in >= C && in % 8 == 0 && in < ((int64_t)1 << 40));
+}
+static bool is_float_type(int t) { return t == PRISM_BF16 || t == PRISM_F32; }
+
+static int check_norm(const prism_norm_params *p) {
+  if (!p) return fail(PRISM_EINVAL, "norm params is NULL");
+  if (p->rows < 0 || p->rows > 0x7fffff00LL) return fail(PRISM_EINVAL, "block_norm: rows must be in [0, 2^31 - 256]");
+  if (p->seqs < 1) return fail(PRISM_EINVAL, "block_norm: seqs must be positive");
+  if (p->seqs > 65535) return fail(PRISM_EINVAL, "block_norm: at most 65535 sequences");
+  if (p->channels < 8 || p->channels % 8 || p->channels > PRISM_NORM_MAX_CHANNELS)
+    return fail(PRISM_EINVAL, "block_norm: channels must be a multiple of 8 in [8, 8192]");
+  if (!is_float_type(p->stream_dtype) || !is_float_type(p->branch_dtype) || !is_float_type(p->param_dtype))
+    return fail(PRISM_EINVAL, "block_norm: dtypes must be bf16 or f32");
+  if (p->post_norm < PRISM_NORM_NONE || p->post_norm > PRISM_NORM_LAYER) return fail(PRISM_EINVAL, "block_norm: unknown post_norm");
+  if (p->pre_norm != PRISM_NORM_RMS && p->pre_norm != PRISM_NORM_LAYER) return fail(PRISM_EINVAL, "block_norm: pre_norm must be RMS or LAYER");
+  if (!(p->eps >= 0.f) || std::isinf(p->eps) || !std::isfinite(p->alpha)) return fail(PRISM_EINVAL, "block_norm: eps must be finite and >= 0, alpha finite");
+  for (int64_t s : {p->gate_stride, p->scale_stride, p->shift_stride})
+    if (s != 0 && (s < p->channels || s % 8 || s >= ((int64_t)1 << 40)))
+      return fail(PRISM_EINVAL, "block_norm: parameter strides must be 0 or a multiple of 8 of at least channels");
+  return PRISM_OK;
+}
+
+static int norm_args(const prism_norm_params *p, const int32_t *off, const void *post_weight, const void *gate,
+                     const void *weight, const void *scale, const void *shift, BlockNormArgs *a) {
+  if (!off && !even_split(p->rows, p->seqs))
+    return fail(PRISM_EINVAL, "block_norm: without offsets the rows must split evenly over the sequences");
+  for (const void *q : {post_weight, gate, weight, scale, shift})
+    if (!aligned16(q)) return fail(PRISM_EINVAL, "block_norm: parameters must be 16-byte aligned");
+  if (!norm_row_stride(p->x_row_stride, p->channels, &a->sx) || !norm_row_stride(p->y_row_stride, p->channels, &a->sy) ||
+      !norm_row_stride(p->x_out_row_stride, p->channels, &a->sxo) || !norm_row_stride(p->h_row_stride, p->channels, &a->sh) ||
+      !norm_row_stride(p->dh_row_stride, p->channels, &a->sdh) || !norm_row_stride(p->dx_out_row_stride, p->channels, &a->sdxo) ||
+      !norm_row_stride(p->dx_row_stride, p->channels, &a->sdx) || !norm_row_stride(p->dy_row_stride, p->channels, &a->sdy))
+    return fail(PRISM_EINVAL, "block_norm: row strides must be 0 or a multiple of 8 of at least channels");
+  a->seq = make_offsets(off, p->seqs, p->rows);
+  a->C = p->channels;
+  a->post = p->post_norm;
+  a->pre = p->pre_norm;
+  a->param_f32 = p->param_dtype == PRISM_F32;
+  a->eps = p->eps;
+  a->alpha = p->alpha;
+  a->post_weight = post_weight;
+  a->gate = gate;
+  a->weight = weight;
+  a->scale = scale;
+  a->shift = shift;
+  a->sgate = p->gate_stride;
+  a->sscale = p->scale_stride;
+  a->sshift = p->shift_stride;
+  a->part = nullptr;
+  a->y_norms = nullptr;
+  a->h = a->x_out = a->dx = a->dy = nullptr;
+  a->x = a->y = a->dh = a->dx_out = nullptr;
+  return PRISM_OK;
+}
+
+// Threads: 8 columns each up to 4096 channels, 16 beyond; narrow rows share a
+// CTA of about 256 threads.
+struct NormShape {
+  int vec, wpr, rpc, threads;
+  explicit NormShape(int C) {
+    vec = C > 8 * kBnMaxThreads ? 2 : 1;
+    wpr = (C + 256 * vec - 1) / (256 * vec);
+    rpc = std::max(1, 8 / wpr);
+    threads = wpr * rpc * 32;
+  }
+};
+static int norm_unit(int64_t rows, int rpc, int slots, int most) {
+  const int64_t u = (rows + slots - 1) / slots;
+  return (int)std::max<int64_t>(rpc, std::min<int64_t>(most, (u + rpc - 1) / rpc * rpc));
+}
+
+struct NormBwdWs {
+  NormShape shape;
+  int unit;
+  int64_t slots;
+  size_t part, sums, total;
+  explicit NormBwdWs(const prism_norm_params *p) : shape(p->channels) {
+    unit = norm_unit(p->rows, shape.rpc, 148 * 2, 1 << 20);
+    slots = slot_bound(p->rows, p->seqs, 1, unit);
+    part = 0;
+    sums = align256((size_t)slots * shape.rpc * 3 * p->channels * 4);
+    total = sums + align256((size_t)p->seqs * 3 * p->channels * 4);
+  }
+};
+
+template <typename TX, typename TY>
+static int launch_norm_fwd(const prism_norm_params *p, BlockNormArgs &a, cudaStream_t st) {
+  const NormShape s(p->channels);
+  a.unit = norm_unit(p->rows, s.rpc, 148 * 8, 32 * s.rpc);
+  const unsigned grid = (unsigned)slot_bound(p->rows, p->seqs, 1, a.unit);
+  if (s.vec == 1)
+    PRISM_TRACED("block_norm_fwd_kernel", st, block_norm_fwd_kernel<TX, TY, 1><<<grid, s.threads, 0, st>>>(a, s.wpr));
+  else
+    PRISM_TRACED("block_norm_fwd_kernel", st, block_norm_fwd_kernel<TX, TY, 2><<<grid, s.threads, 0, st>>>(a, s.wpr));
+  return PRISM_OK;
+}
+template <typename TX, typename TY>
+static int launch_norm_bwd(const NormBwdWs &w, BlockNormArgs &a, cudaStream_t st) {
+  if (w.shape.vec == 1)
+    PRISM_TRACED("block_norm_bwd_kernel", st, block_norm_bwd_kernel<TX, TY, 1><<<(unsigned)w.slots, w.shape.threads, 0, st>>>(a, w.shape.wpr));
+  else
+    PRISM_TRACED("block_norm_bwd_kernel", st, block_norm_bwd_kernel<TX, TY, 2><<<(unsigned)w.slots, w.shape.threads, 0, st>>>(a, w.shape.wpr));
+  return PRISM_OK;
+}
+
+}  // namespace prism
+
+extern "C" {
+
+int prism_packed_workspace_size(const prism_packed_params *p, int kind, size_t *bytes) {
+  int rc = check_packed(p);
+  if (rc) return rc;
+  if (!bytes) return fail(PRISM_EINVAL, "bytes is NULL");
+  switch (kind) {
+    case PRISM_WS_PACKED_FWD: *bytes = 0; break;
+    case PRISM_WS_PACKED_BWD: *bytes = PackedBwdWs(p).total; break;
+    default: return fail(PRISM_EINVAL, "unknown workspace kind");
+  }
+  return PRISM_OK;
+}
+
+int prism_packed_attn_fwd(const prism_packed_params *p, const void *q, const void *k, const void *v,
+                          const int32_t *q_off, const int32_t *k_off, const int32_t *k_used, void *o, void *o_res,
+                          float *lse, void *workspace, size_t ws_bytes, prism_stream stream) {
+  (void)workspace;
+  (void)ws_bytes;
+  int rc = check_packed(p);
+  if (rc) return rc;
+  PackedArgs a = {};
+  rc = packed_args(p, q, k, v, q_off, k_off, k_used, &a);
+  if (rc) return rc;
+  if (p->q_rows == 0) return PRISM_OK;
+  if (!o || !lse) return fail(PRISM_EINVAL, "packed: NULL output");
+  if (!aligned16(o) || !aligned16(o_res)) return fail(PRISM_EINVAL, "packed: tensors must be 16-byte aligned");
+  a.o = static_cast<__nv_bfloat16 *>(o);
+  a.o_res = static_cast<__nv_bfloat16 *>(o_res);
+  a.lse = lse;
+  cudaStream_t st = as_stream(stream);
+  return p->head_dim == 128 ? launch_packed_fwd<128>(p, a, st) : launch_packed_fwd<64>(p, a, st);
+}
+
+int prism_packed_attn_bwd(const prism_packed_params *p, const void *q, const void *k, const void *v, const void *o,
+                          const void *o_res, const void *dout, const float *lse, const int32_t *q_off,
+                          const int32_t *k_off, const int32_t *k_used, void *dq, void *dk, void *dv, void *workspace,
+                          size_t ws_bytes, prism_stream stream) {
+  int rc = check_packed(p);
+  if (rc) return rc;
+  PackedArgs a = {};
+  rc = packed_args(p, q, k, v, q_off, k_off, k_used, &a);
+  if (rc) return rc;
+  if ((p->q_rows && (!o || !dout || !lse || !dq)) || (p->k_rows && (!dk || !dv)))
+    return fail(PRISM_EINVAL, "packed: NULL tensor");
+  for (const void *t : {o, o_res, dout, (const void *)dq, (const void *)dk, (const void *)dv})
+    if (!aligned16(t)) return fail(PRISM_EINVAL, "packed: tensors must be 16-byte aligned");
+  if (!fill_strides(p->dout_stride, p->q_rows, p->heads, p->head_dim, false, a.sdo) ||
+      !fill_strides(p->dq_stride, p->q_rows, p->heads, p->head_dim, true, a.sdq) ||
+      !fill_strides(p->dk_stride, p->k_rows, p->kv_heads, p->head_dim, true, a.sdk) ||
+      !fill_strides(p->dv_stride, p->k_rows, p->kv_heads, p->head_dim, true, a.sdv))
+    return fail(PRISM_EINVAL, "packed: strides must be positive multiples of 8, and outputs must not overlap themselves");
+  const PackedBwdWs w(p);
+  if (w.total && (!workspace || ws_bytes < w.total || !aligned16(workspace)))
+    return fail(PRISM_EINVAL, "packed: workspace missing, misaligned or below prism_packed_workspace_size");
+  uint8_t *ws = static_cast<uint8_t *>(workspace);
+  float *delta = reinterpret_cast<float *>(ws + w.delta), *lse2 = reinterpret_cast<float *>(ws + w.lse2);
+  a.o = static_cast<__nv_bfloat16 *>(const_cast<void *>(o));
+  a.o_res = static_cast<__nv_bfloat16 *>(const_cast<void *>(o_res));
+  a.dout = static_cast<const __nv_bfloat16 *>(dout);
+  a.lse = const_cast<float *>(lse);
+  a.delta = delta;
+  a.lse2 = lse2;
+  a.dq = static_cast<__nv_bfloat16 *>(dq);
+  a.dk = static_cast<__nv_bfloat16 *>(dk);
+  a.dv = static_cast<__nv_bfloat16 *>(dv);
+  cudaStream_t st = as_stream(stream);
+  return p->head_dim == 128 ? launch_packed_bwd<128>(p, a, delta, lse2, st) : launch_packed_bwd<64>(p, a, delta, lse2, st);
+}
+
+int prism_block_norm_fwd(const prism_norm_params *p, const void *x, const void *y, const int32_t *off,
+                         const void *post_weight, const void *gate, const void *weight, const void *scale,
+                         const void *shift, void *x_out, void *h, float *y_norms, prism_stream stream) {
+  int rc = check_norm(p);
+  if (rc) return rc;
+  BlockNormArgs a;
+  rc = norm_args(p, off, post_weight, gate, weight, scale, shift, &a);
+  if (rc) return rc;
+  if (p->rows == 0) return PRISM_OK;
+  if (!x || (y && !x_out) || (!y && !h)) return fail(PRISM_EINVAL, "block_norm: NULL tensor");
+  if (!y && y_norms) return fail(PRISM_EINVAL, "block_norm: y_norms needs y");
+  for (const void *t : {x, y, (const void *)x_out, (const void *)h})
+    if (!aligned16(t)) return fail(PRISM_EINVAL, "block_norm: tensors must be 16-byte aligned");
+  a.x = x;
+  a.y = y;
+  a.x_out = y ? x_out : nullptr;
+  a.h = h;
+  a.y_norms = y_norms;
+  cudaStream_t st = as_stream(stream);
+  if (p->stream_dtype == PRISM_BF16)
+    return p->branch_dtype == PRISM_BF16 ? launch_norm_fwd<__nv_bfloat16, __nv_bfloat16>(p, a, st)
+                                         : launch_norm_fwd<__nv_bfloat16, float>(p, a, st);
+  return p->branch_dtype == PRISM_BF16 ? launch_norm_fwd<float, __nv_bfloat16>(p, a, st)
+                                       : launch_norm_fwd<float, float>(p, a, st);
+}
+
+int prism_block_norm_workspace_size(const prism_norm_params *p, size_t *bytes) {
+  int rc = check_norm(p);
+  if (rc) return rc;
+  if (!bytes) return fail(PRISM_EINVAL, "bytes is NULL");
+  *bytes = NormBwdWs(p).total;
+  return PRISM_OK;
+}
+
+int prism_block_norm_bwd(const prism_norm_params *p, const void *x_out, const void *y, const int32_t *off,
+                         const void *post_weight, const void *gate, const void *weight, const void *scale,
+                         const void *dh, const void *dx_out, void *dx, void *dy, void *dpost_weight, void *dgate,
+                         void *dweight, void *dscale, void *dshift, void *workspace, size_t ws_bytes,
+                         prism_stream stream) {
+  int rc = check_norm(p);
+  if (rc) return rc;
+  BlockNormArgs a;
+  rc = norm_args(p, off, post_weight, gate, weight, scale, nullptr, &a);
+  if (rc) return rc;
+  if (p->rows && ((!dh && !dx_out) || (dh && !x_out) || !dx || (y && !dy)))
+    return fail(PRISM_EINVAL, "block_norm: NULL tensor");
+  if (!y && (dpost_weight || dgate)) return fail(PRISM_EINVAL, "block_norm: dpost_weight and dgate need y");
+  for (const void *t : {x_out, y, dh, dx_out, (const void *)dx, (const void *)dy})
+    if (!aligned16(t)) return fail(PRISM_EINVAL, "block_norm: tensors must be 16-byte aligned");
+  const NormBwdWs w(p);
+  if (!workspace || ws_bytes < w.total || !aligned16(workspace))
+    return fail(PRISM_EINVAL, "block_norm: workspace missing, misaligned or below prism_block_norm_workspace_size");
+  uint8_t *ws = static_cast<uint8_t *>(workspace);
+  const bool want = dpost_weight || dgate || dweight || dscale || dshift;
+  a.unit = w.unit;
+  a.y = y;
+  a.x_out = const_cast<void *>(x_out);
+  a.dh = dh;
+  a.dx_out = dx_out;
+  a.dx = dx;
+  a.dy = dy;
+  a.part = want ? reinterpret_cast<float *>(ws + w.part) : nullptr;
+  cudaStream_t st = as_stream(stream);
+  if (p->rows) {
+    if (p->stream_dtype == PRISM_BF16)
+      rc = p->branch_dtype == PRISM_BF16 ? launch_norm_bwd<__nv_bfloat16, __nv_bfloat16>(w, a, st)
+                                         : launch_norm_bwd<__nv_bfloat16, float>(w, a, st);
+    else
+      rc = p->branch_dtype == PRISM_BF16 ? launch_norm_bwd<float, __nv_bfloat16>(w, a, st)
+                                         : launch_norm_bwd<float, float>(w, a, st);
+    if (rc) return rc;
+  }
+  if (!want) return PRISM_OK;
+  BnParamArgs q = {};
+  q.seq = a.seq;
+  q.C = a.C;
+  q.unit = w.unit;
+  q.rpc = w.shape.rpc;
+  q.param_f32 = a.param_f32;
+  q.part = a.part;
+  q.sums = reinterpret_cast<float *>(ws + w.sums);
+  q.weight = weight;
+  q.post_weight = post_weight;
+  q.gate = gate;
+  q.scale = scale;
+  q.sgate = a.sgate;
+  q.sscale = a.sscale;
+  q.dweight = dweight;
+  q.dpost_weight = dpost_weight;
+  q.dgate = dgate;
+  q.dscale = dscale;
+  q.dshift = dshift;
+  q.per_gate = p->gate_stride != 0;
+  q.per_scale = p->scale_stride != 0;
+  q.per_shift = p->shift_stride != 0;
+  PRISM_TRACED("block_norm_sums_kernel", st, block_norm_sums_kernel<<<dim3((unsigned)((a.C + 31) / 32), p->seqs), 1024, 0, st>>>(q));
+  if (dweight || dpost_weight || (dscale && !q.per_scale) || (dshift && !q.per_shift) || (dgate && !q.per_gate))
+    PRISM_TRACED("block_norm_params_kernel", st, block_norm_params_kernel<<<(unsigned)((a.C + 127) / 128), 128, 0, st>>>(q));
+  return PRISM_OK;
+}
+
+}  // extern "C"

@@ -742,3 +742,5 @@ int prism_bsa_bwd(const prism_params *p, const prism_block *blocks, const int32_
 }
 
 }  // extern "C"
+
+#include "packed_host.cuh"

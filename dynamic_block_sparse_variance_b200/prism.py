@@ -19,6 +19,8 @@ LIB_PATH = os.path.join(_HERE, "libprism_b200.so")
 PRISM_OK, PRISM_EINVAL, PRISM_ECAPACITY, PRISM_ECUDA, PRISM_ETIMEOUT, PRISM_EBOUNDS = 0, -1, -2, -3, -4, -5
 PRISM_BF16, PRISM_F32 = 0, 1
 PRISM_WS_INDICATOR, PRISM_WS_SELECT, PRISM_WS_FWD, PRISM_WS_BWD = 0, 1, 2, 3
+PRISM_WS_PACKED_FWD, PRISM_WS_PACKED_BWD = 4, 5
+PRISM_NORM_NONE, PRISM_NORM_RMS, PRISM_NORM_LAYER = 0, 1, 2
 PRISM_OPT_ATTN_BACKEND, PRISM_OPT_WAIT_LIMIT, PRISM_OPT_DEBUG_STALL = 0, 1, 2
 
 # Entry points declared in include/prism.h, in declaration order.
@@ -26,6 +28,8 @@ ENTRY_POINTS = (
     "prism_workspace_size", "prism_audio_norms", "prism_zone_records", "prism_zone_finalize", "prism_zone_indicator", "prism_zone_indicator_noalloc", "prism_assign_blocks",
     "prism_permute",
     "prism_unpermute", "prism_block_select", "prism_bsa_fwd", "prism_bsa_bwd",
+    "prism_packed_workspace_size", "prism_packed_attn_fwd", "prism_packed_attn_bwd",
+    "prism_block_norm_fwd", "prism_block_norm_workspace_size", "prism_block_norm_bwd",
     "prism_set_option", "prism_set_trace", "prism_device_status", "prism_last_error",
 )
 
@@ -62,6 +66,23 @@ def make_params(T, H, W, heads, head_dim, top_k, top_p, tau128=0.5, tau256=0.25,
     return prism_params(T, H, W, heads, head_dim, tau128, tau256, eps, top_k, top_p, scale, fixed_shape, sparsity)
 
 
+class prism_packed_params(ctypes.Structure):
+    _fields_ = [("seqs", ctypes.c_int32), ("heads", ctypes.c_int32), ("kv_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("q_rows", ctypes.c_int64), ("k_rows", ctypes.c_int64),
+                ("causal", ctypes.c_int32), ("scale", ctypes.c_float)] + \
+               [(n + "_stride", ctypes.c_int64 * 2) for n in ("q", "k", "v", "o", "dout", "dq", "dk", "dv")]
+
+
+class prism_norm_params(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("channels", ctypes.c_int32), ("seqs", ctypes.c_int32),
+                ("stream_dtype", ctypes.c_int32), ("branch_dtype", ctypes.c_int32), ("param_dtype", ctypes.c_int32),
+                ("post_norm", ctypes.c_int32), ("pre_norm", ctypes.c_int32), ("eps", ctypes.c_float),
+                ("alpha", ctypes.c_float)] + \
+               [(n, ctypes.c_int64) for n in ("gate_stride", "scale_stride", "shift_stride", "x_row_stride",
+                                              "y_row_stride", "x_out_row_stride", "h_row_stride", "dh_row_stride",
+                                              "dx_out_row_stride", "dx_row_stride", "dy_row_stride")]
+
+
 _lib = None
 _P = ctypes.c_void_p
 
@@ -89,6 +110,12 @@ def lib():
             "prism_bsa_fwd": [pp, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, sz, _P],
             "prism_bsa_bwd": [pp, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, i64, _P, _P, _P,
                               _P, sz, _P],
+            "prism_packed_workspace_size": [_P, ctypes.c_int, ctypes.POINTER(sz)],
+            "prism_packed_attn_fwd": [_P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, sz, _P],
+            "prism_packed_attn_bwd": [_P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, sz, _P],
+            "prism_block_norm_fwd": [_P] * 13,
+            "prism_block_norm_workspace_size": [_P, ctypes.POINTER(sz)],
+            "prism_block_norm_bwd": [_P] * 18 + [sz, _P],
             "prism_set_option": [ctypes.c_int, i64],
             "prism_set_trace": [TRACE_FN, _P],
             "prism_device_status": [_P],
@@ -196,6 +223,44 @@ def prism_bsa_bwd(p, blocks, zone_blk_base, nblk, q, k, v, o, o_res, dout, lse, 
                                _ptr(k), _ptr(v), _ptr(o), _ptr(o_res), _ptr(dout), _ptr(lse), _ptr(row_ptr),
                                _ptr(col), _ptr(nnz), col.numel(), _ptr(dq), _ptr(dk), _ptr(dv),
                                _ptr(workspace), workspace.numel(), _stream()))
+
+
+def prism_packed_workspace_size(p, kind):
+    n = ctypes.c_size_t(0)
+    _check(lib().prism_packed_workspace_size(ctypes.byref(p), kind, ctypes.byref(n)))
+    return n.value
+
+
+def prism_packed_attn_fwd(p, q, k, v, q_off, k_off, k_used, o, o_res, lse, workspace=None):
+    _check(lib().prism_packed_attn_fwd(ctypes.byref(p), _ptr(q), _ptr(k), _ptr(v), _ptr(q_off), _ptr(k_off),
+                                       _ptr(k_used), _ptr(o), _ptr(o_res), _ptr(lse), _ptr(workspace),
+                                       0 if workspace is None else workspace.numel(), _stream()))
+
+
+def prism_packed_attn_bwd(p, q, k, v, o, o_res, dout, lse, q_off, k_off, k_used, dq, dk, dv, workspace=None):
+    _check(lib().prism_packed_attn_bwd(ctypes.byref(p), _ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(o_res), _ptr(dout),
+                                       _ptr(lse), _ptr(q_off), _ptr(k_off), _ptr(k_used), _ptr(dq), _ptr(dk), _ptr(dv),
+                                       _ptr(workspace), 0 if workspace is None else workspace.numel(), _stream()))
+
+
+def prism_block_norm_workspace_size(p):
+    n = ctypes.c_size_t(0)
+    _check(lib().prism_block_norm_workspace_size(ctypes.byref(p), ctypes.byref(n)))
+    return n.value
+
+
+def prism_block_norm_fwd(p, x, y, off, post_weight, gate, weight, scale, shift, x_out, h, y_norms=None):
+    _check(lib().prism_block_norm_fwd(ctypes.byref(p), _ptr(x), _ptr(y), _ptr(off), _ptr(post_weight), _ptr(gate),
+                                      _ptr(weight), _ptr(scale), _ptr(shift), _ptr(x_out), _ptr(h), _ptr(y_norms),
+                                      _stream()))
+
+
+def prism_block_norm_bwd(p, x_out, y, off, post_weight, gate, weight, scale, dh, dx_out, dx, dy, dpost_weight, dgate,
+                         dweight, dscale, dshift, workspace):
+    _check(lib().prism_block_norm_bwd(ctypes.byref(p), _ptr(x_out), _ptr(y), _ptr(off), _ptr(post_weight), _ptr(gate),
+                                      _ptr(weight), _ptr(scale), _ptr(dh), _ptr(dx_out), _ptr(dx), _ptr(dy),
+                                      _ptr(dpost_weight), _ptr(dgate), _ptr(dweight), _ptr(dscale), _ptr(dshift),
+                                      _ptr(workspace), workspace.numel(), _stream()))
 
 
 def prism_set_option(option, value):

@@ -311,6 +311,147 @@ int prism_bsa_bwd(const prism_params *p, const prism_block *blocks, const int32_
                   const int64_t *nnz, int64_t col_capacity, void *dq, void *dk, void *dv,
                   void *workspace, size_t ws_bytes, prism_stream stream);
 
+/* ---------------------------------------------------------------------------
+ * Packed sequences.  The layers around the block-sparse one work on batches of
+ * sequences of different lengths (samples, prompts, conditioning tokens)
+ * stored one behind the other in the rows of one tensor.  Sequence b holds rows
+ * [off[b], off[b+1]); `off` is a DEVICE array of seqs + 1 int32, ascending and
+ * within the tensor.  A NULL `off` splits the rows evenly.  Rows outside every
+ * sequence are not written and reach no result.  Offsets that leave the tensor or run
+ * backwards latch PRISM_EBOUNDS; their sequences are treated as empty.
+ */
+
+/*
+ * Dense softmax attention over packed sequences, with grouped heads: query
+ * head h reads key/value head h / (heads / kv_heads).
+ *   seqs               sequences, >= 1
+ *   heads, kv_heads    heads a multiple of kv_heads, at most 128 per kv head
+ *   head_dim           64 or 128
+ *   q_rows, k_rows     rows of q, o, dout, dq and of k, v, dk, dv (< 2^31)
+ *   causal             0: every query sees every key of its sequence.  1: with lq
+ *                      queries and lk keys, query i sees keys 0 .. i + lk - lq
+ *                      (the last query sees them all; with lq > lk the first
+ *                      lq - lk queries see none)
+ *   scale              softmax scale; 0 means 1/sqrt(head_dim)
+ *   *_stride           {row, head} strides in elements, for tensors that are
+ *                      slices of larger ones; multiples of 8, the elements of
+ *                      a head consecutive.  {0, 0} means contiguous
+ *                      [rows, heads, head_dim].
+ */
+typedef struct {
+  int32_t seqs;
+  int32_t heads, kv_heads, head_dim;
+  int64_t q_rows, k_rows;
+  int32_t causal;
+  float scale;
+  int64_t q_stride[2], k_stride[2], v_stride[2], o_stride[2];
+  int64_t dout_stride[2], dq_stride[2], dk_stride[2], dv_stride[2];
+} prism_packed_params;
+
+#define PRISM_WS_PACKED_FWD 4
+#define PRISM_WS_PACKED_BWD 5
+
+/* Bytes of workspace of prism_packed_attn_fwd / _bwd (kind = PRISM_WS_PACKED_*).
+ * Host-only; depends on the sizes, not on the pointers. */
+int prism_packed_workspace_size(const prism_packed_params *p, int kind, size_t *bytes);
+
+/*
+ * Forward: O_r = softmax(scale q_r K^T) V over the keys that row r sees, and
+ * LSE_r, the natural log of the sum of their exponentials.  A row that sees no
+ * key gets O = 0 and LSE = -inf.
+ *   q, k, v        bf16, 16-byte aligned
+ *   q_off, k_off   [seqs + 1] row offsets, nullable (an even split)
+ *   k_used         [seqs] int32, nullable: only the first k_used[b] rows of
+ *                  sequence b's key rows are in use (a cache with room); rows
+ *                  behind them may hold anything.
+ *   o              out bf16; o_res out, nullable: bf16 contiguous
+ *                  [q_rows, heads, head_dim], the rounding residual of O, for
+ *                  the backward (see prism_bsa_fwd)
+ *   lse            out float [heads, q_rows]
+ * Values within a sequence have to be finite: a masked (future) key's value
+ * is multiplied by zero.  What lies outside the sequences, or behind k_used, does
+ * not reach any result.  Results do not change from run to run.
+ */
+int prism_packed_attn_fwd(const prism_packed_params *p, const void *q, const void *k, const void *v,
+                          const int32_t *q_off, const int32_t *k_off, const int32_t *k_used, void *o,
+                          void *o_res, float *lse, void *workspace, size_t ws_bytes, prism_stream stream);
+
+/*
+ * Backward of prism_packed_attn_fwd: dq, dk, dv (bf16) from dout (bf16), o, lse
+ * and, nullable, o_res.  dk and dv sum over the query heads of a group; key
+ * rows that no query sees, and rows behind k_used, get zero.  Results do
+ * not change from run to run.
+ */
+int prism_packed_attn_bwd(const prism_packed_params *p, const void *q, const void *k, const void *v,
+                          const void *o, const void *o_res, const void *dout, const float *lse,
+                          const int32_t *q_off, const int32_t *k_off, const int32_t *k_used, void *dq,
+                          void *dk, void *dv, void *workspace, size_t ws_bytes, prism_stream stream);
+
+/*
+ * The norms around a block, fused with its gate and the residual stream:
+ *   x_out = alpha x + gate (N_post(y) post_weight)
+ *   h     = N_pre(x_out) weight (1 + scale) + shift
+ * with N one of PRISM_NORM_NONE (the identity), PRISM_NORM_RMS
+ * (z / sqrt(mean(z^2) + eps)) and PRISM_NORM_LAYER (the same of z - mean(z)).
+ *   rows, channels   [rows, channels] tensors; channels a multiple of 8, at
+ *                    most PRISM_NORM_MAX_CHANNELS
+ *   seqs             packed sequences (see above): gate, scale and shift have a
+ *                    row per sequence
+ *   stream_dtype     of x, x_out, dx, dx_out;  branch_dtype  of y, h, dy, dh;
+ *   param_dtype      of weights, gate, scale, shift and their gradients
+ *                    (each PRISM_BF16 or PRISM_F32)
+ *   post_norm        any;  pre_norm  RMS or LAYER
+ *   gate_stride, scale_stride, shift_stride   elements from one sequence's row to
+ *                    the next (slices of one modulation tensor); 0: one row
+ *                    shared by all sequences.  Multiples of 8.
+ *   *_row_stride     elements from one row to the next of each tensor, multiples
+ *                    of 8; 0 means channels
+ * Statistics and sums are formed in float.
+ */
+#define PRISM_NORM_NONE 0
+#define PRISM_NORM_RMS 1
+#define PRISM_NORM_LAYER 2
+#define PRISM_NORM_MAX_CHANNELS 8192
+typedef struct {
+  int64_t rows;
+  int32_t channels, seqs;
+  int32_t stream_dtype, branch_dtype, param_dtype;
+  int32_t post_norm, pre_norm;
+  float eps, alpha;
+  int64_t gate_stride, scale_stride, shift_stride;
+  int64_t x_row_stride, y_row_stride, x_out_row_stride, h_row_stride;
+  int64_t dh_row_stride, dx_out_row_stride, dx_row_stride, dy_row_stride;
+} prism_norm_params;
+
+/*
+ * Forward.  y NULL: the norm before a block alone (h from x; alpha, gate and
+ * x_out are not used).  h NULL: the norm after a block alone (x_out).  Weights,
+ * gate, scale and shift are nullable (1, 1, 0, 0).
+ *   y_norms   out, nullable: [rows] float ||y_n||_2, the indicator's audio
+ *             input when y is the audio-to-video cross-attention's output
+ *             (Method §1; what prism_audio_norms computes in a pass of its own)
+ */
+int prism_block_norm_fwd(const prism_norm_params *p, const void *x, const void *y, const int32_t *off,
+                         const void *post_weight, const void *gate, const void *weight, const void *scale,
+                         const void *shift, void *x_out, void *h, float *y_norms, prism_stream stream);
+
+/* Bytes of workspace of prism_block_norm_bwd.  Host-only. */
+int prism_block_norm_workspace_size(const prism_norm_params *p, size_t *bytes);
+
+/*
+ * Backward: from dh (nullable: no h) and dx_out (nullable: zero), dx and, with
+ * y, dy; and the gradients of the parameters, each nullable (not wanted).  x_out
+ * and y are the forward's (without y: x_out is x).  dgate, dscale and dshift are
+ * [seqs, channels] contiguous, or [channels] where the stride is 0 (the sum over
+ * the sequences); all in param_dtype, summed in float in a fixed order.
+ *   workspace  >= prism_block_norm_workspace_size() bytes
+ */
+int prism_block_norm_bwd(const prism_norm_params *p, const void *x_out, const void *y, const int32_t *off,
+                         const void *post_weight, const void *gate, const void *weight, const void *scale,
+                         const void *dh, const void *dx_out, void *dx, void *dy, void *dpost_weight,
+                         void *dgate, void *dweight, void *dscale, void *dshift, void *workspace,
+                         size_t ws_bytes, prism_stream stream);
+
 /* Process-wide options (host-only; set while no call is in flight).
  *   PRISM_OPT_ATTN_BACKEND  0 (default): tcgen05/TMEM/TMA attention kernels for
  *                           head_dim 128, warp-level MMA kernels otherwise;
