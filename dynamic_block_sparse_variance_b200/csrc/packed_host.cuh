@@ -3,6 +3,7 @@
 #pragma once
 
 #include "block_norm.cuh"
+#include "packed_fwd_tc.cuh"
 #include "packed_simple.cuh"
 
 namespace prism {
@@ -34,6 +35,8 @@ static int check_packed(const prism_packed_params *p) {
   if (p->head_dim != 64 && p->head_dim != 128) return fail(PRISM_EINVAL, "packed: head_dim must be 64 or 128");
   if (p->q_rows < 0 || p->k_rows < 0 || p->q_rows > 0x7fffff00LL || p->k_rows > 0x7fffff00LL)
     return fail(PRISM_EINVAL, "packed: row counts must be in [0, 2^31 - 256]");
+  if (p->q_rows * (p->heads / p->kv_heads) > 0x7fffff00LL)
+    return fail(PRISM_EINVAL, "packed: q_rows * heads / kv_heads must stay below 2^31 - 256");
   if (!(p->scale >= 0.f) || std::isinf(p->scale)) return fail(PRISM_EINVAL, "packed: scale must be finite and >= 0");
   return PRISM_OK;
 }
@@ -79,11 +82,61 @@ struct PackedBwdWs {
   }
 };
 
+// 3-D map (head_dim, head, row) over a strided tensor: boxes of 64 columns of
+// one head of 128 rows, 128-byte swizzle; rows past the end read as zero.
+static bool make_head_map(CUtensorMap *map, const void *base, int D, int heads, int64_t rows, const int64_t s[2],
+                          cuuint32_t box_heads = 1, cuuint32_t box_rows = 128) {
+  auto enc = tensor_map_encoder();
+  if (!enc) return false;
+  cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)heads, (cuuint64_t)rows};
+  cuuint64_t strides[2] = {(cuuint64_t)s[1] * 2, (cuuint64_t)s[0] * 2};
+  cuuint32_t box[3] = {64, box_heads, box_rows};
+  cuuint32_t estr[3] = {1, 1, 1};
+  return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides, box, estr,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+static uint32_t wait_limit() { return g_wait_limit ? g_wait_limit : kDefaultWaitLimit; }
+
+// How the forward's keys are split: over about as many CTAs as there are SMs
+// when the query rows alone give fewer, with at least 512 keys a share.  The
+// host knows the rows, not the sequences' lengths, and goes by their average.
+struct PackedFwdWs {
+  int splits;
+  size_t o, lse2, total;
+  explicit PackedFwdWs(const prism_packed_params *p) {
+    const int64_t group = p->heads / p->kv_heads;
+    const int64_t ctas = std::max<int64_t>(1, std::max<int64_t>(p->seqs, p->q_rows * group / 256) * p->kv_heads);
+    const int64_t keys = p->k_rows / p->seqs;
+    splits = (int)std::max<int64_t>(1, std::min<int64_t>({148 / ctas, keys / 512, 64}));
+    const size_t n = (size_t)p->q_rows * p->heads;
+    o = 0;
+    lse2 = splits > 1 ? align256(n * splits * p->head_dim * 4) : 0;
+    total = splits > 1 ? lse2 + align256(n * splits * 4) : 0;
+  }
+};
+
 template <int D>
-static int launch_packed_fwd(const prism_packed_params *p, const PackedArgs &a, cudaStream_t st) {
-  if (p->q_rows == 0) return PRISM_OK;
-  const dim3 grid((unsigned)slot_bound(p->q_rows, p->seqs, a.group, 8), a.kv_heads);
-  PRISM_TRACED("packed_fwd_simple_kernel", st, packed_fwd_simple_kernel<D><<<grid, 256, 0, st>>>(a));
+static int launch_packed_fwd(const prism_packed_params *p, const PackedArgs &a, uint8_t *ws, cudaStream_t st) {
+  const PackedFwdWs w(p);
+  PackedSplit sp{w.splits, reinterpret_cast<float *>(ws + w.o), reinterpret_cast<float *>(ws + w.lse2)};
+  CUtensorMap tk, tv;
+  // without keys nothing is loaded: the maps then only need to be well formed
+  const bool keys = p->k_rows > 0;
+  const int64_t dummy[2] = {D, D};
+  if (!make_head_map(&tk, keys ? (const void *)a.k : a.q, D, keys ? a.kv_heads : 1, keys ? p->k_rows : 1, keys ? a.sk : dummy) ||
+      !make_head_map(&tv, keys ? (const void *)a.v : a.q, D, keys ? a.kv_heads : 1, keys ? p->k_rows : 1, keys ? a.sv : dummy))
+    return fail(PRISM_ECUDA, "cuTensorMapEncodeTiled failed");
+  cudaFuncSetAttribute(packed_fwd_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, PfCfg<D>::kSmem);
+  const int64_t slots = slot_bound(p->q_rows, p->seqs, a.group, 256);
+  if (slots * a.kv_heads > 0x7fffffffLL) return fail(PRISM_EINVAL, "packed: too many query rows");
+  const dim3 grid((unsigned)(slots * a.kv_heads), 1, w.splits);
+  PRISM_TRACED("packed_fwd_tc_kernel", st, packed_fwd_tc_kernel<D><<<grid, kPfThreads, PfCfg<D>::kSmem, st>>>(tk, tv, a, sp, wait_limit()));
+  if (w.splits > 1) {
+    const int64_t threads = p->q_rows * p->heads * (D / 4);
+    PRISM_TRACED("packed_combine_kernel", st, packed_combine_kernel<D><<<(unsigned)((threads + 255) / 256), 256, 0, st>>>(a, sp));
+  }
   return PRISM_OK;
 }
 
@@ -221,7 +274,7 @@ int prism_packed_workspace_size(const prism_packed_params *p, int kind, size_t *
   if (rc) return rc;
   if (!bytes) return fail(PRISM_EINVAL, "bytes is NULL");
   switch (kind) {
-    case PRISM_WS_PACKED_FWD: *bytes = 0; break;
+    case PRISM_WS_PACKED_FWD: *bytes = PackedFwdWs(p).total; break;
     case PRISM_WS_PACKED_BWD: *bytes = PackedBwdWs(p).total; break;
     default: return fail(PRISM_EINVAL, "unknown workspace kind");
   }
@@ -231,8 +284,6 @@ int prism_packed_workspace_size(const prism_packed_params *p, int kind, size_t *
 int prism_packed_attn_fwd(const prism_packed_params *p, const void *q, const void *k, const void *v,
                           const int32_t *q_off, const int32_t *k_off, const int32_t *k_used, void *o, void *o_res,
                           float *lse, void *workspace, size_t ws_bytes, prism_stream stream) {
-  (void)workspace;
-  (void)ws_bytes;
   int rc = check_packed(p);
   if (rc) return rc;
   PackedArgs a = {};
@@ -244,8 +295,12 @@ int prism_packed_attn_fwd(const prism_packed_params *p, const void *q, const voi
   a.o = static_cast<__nv_bfloat16 *>(o);
   a.o_res = static_cast<__nv_bfloat16 *>(o_res);
   a.lse = lse;
+  const size_t need = PackedFwdWs(p).total;
+  if (need && (!workspace || ws_bytes < need || !aligned16(workspace)))
+    return fail(PRISM_EINVAL, "packed: workspace missing, misaligned or below prism_packed_workspace_size");
   cudaStream_t st = as_stream(stream);
-  return p->head_dim == 128 ? launch_packed_fwd<128>(p, a, st) : launch_packed_fwd<64>(p, a, st);
+  uint8_t *ws = static_cast<uint8_t *>(workspace);
+  return p->head_dim == 128 ? launch_packed_fwd<128>(p, a, ws, st) : launch_packed_fwd<64>(p, a, ws, st);
 }
 
 int prism_packed_attn_bwd(const prism_packed_params *p, const void *q, const void *k, const void *v, const void *o,

@@ -21,47 +21,6 @@ __device__ __forceinline__ float dot(const float (&a)[D / 32], const float (&b)[
 }
 
 template <int D>
-__global__ void __launch_bounds__(256) packed_fwd_simple_kernel(const PackedArgs a) {
-  const int lane = threadIdx.x & 31;
-  const int kvh = blockIdx.y;
-  int64_t piece;
-  PackedSeq::check(a, blockIdx.x);
-  const int b = find_sequence(a.qs, blockIdx.x, a.group, 8, piece);
-  PackedSeq s;
-  if (!s.load(a, b)) return;
-  const int64_t fr = piece * 8 + (threadIdx.x >> 5);
-  if (piece < 0 || fr >= (int64_t)s.lq * a.group) return;
-  const int tok = (int)(fr / a.group), head = kvh * a.group + (int)(fr % a.group);
-  float q[D / 32], k[D / 32], v[D / 32], o[D / 32];
-  load_row<D>(a.q + (int64_t)(s.q0 + tok) * a.sq[0] + head * a.sq[1], q);
-#pragma unroll
-  for (int e = 0; e < D / 32; ++e) o[e] = 0.f;
-  float m = -INFINITY, l = 0.f;
-  const int n = s.visible(a, tok);
-  for (int j = 0; j < n; ++j) {
-    load_row<D>(a.k + (int64_t)(s.k0 + j) * a.sk[0] + kvh * a.sk[1], k);
-    load_row<D>(a.v + (int64_t)(s.k0 + j) * a.sv[0] + kvh * a.sv[1], v);
-    const float x = dot<D>(q, k) * a.scale_log2;
-    const float mn = fmaxf(m, x), c = exp2f(m - mn), p = exp2f(x - mn);
-    l = l * c + p;
-#pragma unroll
-    for (int e = 0; e < D / 32; ++e) o[e] = fmaf(p, v[e], o[e] * c);
-    m = mn;
-  }
-  const float inv = l > 0.f ? 1.f / l : 0.f;
-#pragma unroll
-  for (int e = 0; e < D / 32; ++e) {
-    const float x = o[e] * inv;
-    const __nv_bfloat16 r = __float2bfloat16_rn(x);
-    a.o[(int64_t)(s.q0 + tok) * a.so[0] + head * a.so[1] + lane * (D / 32) + e] = r;
-    if (a.o_res)
-      a.o_res[((int64_t)(s.q0 + tok) * a.heads + head) * D + lane * (D / 32) + e] =
-          __float2bfloat16_rn(x - __bfloat162float(r));
-  }
-  if (lane == 0) a.lse[(int64_t)head * a.qs.rows + s.q0 + tok] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
-}
-
-template <int D>
 __global__ void __launch_bounds__(256) packed_dq_simple_kernel(const PackedArgs a) {
   const int lane = threadIdx.x & 31;
   const int kvh = blockIdx.y;

@@ -318,7 +318,8 @@ int prism_bsa_bwd(const prism_params *p, const prism_block *blocks, const int32_
  * [off[b], off[b+1]); `off` is a DEVICE array of seqs + 1 int32, ascending and
  * within the tensor.  A NULL `off` splits the rows evenly.  Rows outside every
  * sequence are not written and reach no result.  Offsets that leave the tensor or run
- * backwards latch PRISM_EBOUNDS; their sequences are treated as empty.
+ * backwards latch PRISM_EBOUNDS, and the rows of such sequences are unspecified
+ * (nothing outside the tensors is touched).
  */
 
 /*
@@ -327,7 +328,8 @@ int prism_bsa_bwd(const prism_params *p, const prism_block *blocks, const int32_
  *   seqs               sequences, >= 1
  *   heads, kv_heads    heads a multiple of kv_heads, at most 128 per kv head
  *   head_dim           64 or 128
- *   q_rows, k_rows     rows of q, o, dout, dq and of k, v, dk, dv (< 2^31)
+ *   q_rows, k_rows     rows of q, o, dout, dq and of k, v, dk, dv; k_rows and
+ *                      q_rows heads / kv_heads at most 2^31 - 256
  *   causal             0: every query sees every key of its sequence.  1: with lq
  *                      queries and lk keys, query i sees keys 0 .. i + lk - lq
  *                      (the last query sees them all; with lq > lk the first

@@ -85,7 +85,7 @@ def test_block_norm_reference_gradients_against_differences(post, pre, shared):
 @pytest.mark.parametrize("bad,what", [
     (dict(seqs=0), "seqs"), (dict(heads=3), "multiple"), (dict(kv_heads=0), "multiple"), (dict(head_dim=96), "head_dim"),
     (dict(heads=258, kv_heads=2), "128"), (dict(q_rows=-1), "row counts"), (dict(k_rows=2**31), "row counts"),
-    (dict(scale=-1.0), "scale"), (dict(scale=float("nan")), "scale"), (dict(scale=float("inf")), "scale")])
+    (dict(q_rows=2**30), "2\\^31"), (dict(scale=-1.0), "scale"), (dict(scale=float("nan")), "scale"), (dict(scale=float("inf")), "scale")])
 def test_packed_params_refused(lib, bad, what):
     for kind in (P.PRISM_WS_PACKED_FWD, P.PRISM_WS_PACKED_BWD):
         with pytest.raises(P.PrismError, match=what) as e:
