@@ -18,7 +18,7 @@ struct PackedArgs {
   const __nv_bfloat16 *q, *k, *v, *dout;
   __nv_bfloat16 *o, *o_res, *dq, *dk, *dv;
   float *lse;
-  const float *lse2, *delta;        // backward: LSE log2e and rowsum(dO o O), [heads, q_rows]
+  const float *lse2, *delta;        // backward: LSE log2e and rowsum(dO o O), [kv_heads][q_rows][group]
   int64_t sq[2], sk[2], sv[2], so[2], sdo[2], sdq[2], sdk[2], sdv[2];
 };
 
@@ -49,7 +49,7 @@ struct PackedSeq {
 
 // Per query row and head (half a warp for head_dim 64, a warp for 128): D =
 // rowsum(dO o (O + residual)) and LSE log2e; a row that sees nothing gets +inf,
-// so that its probabilities 2^(x - inf) are zero.
+// so that its probabilities 2^(x - inf) are zero.  Written in flattened order.
 template <int D>
 __global__ void __launch_bounds__(256) packed_stats_kernel(const PackedArgs a, const __nv_bfloat16 *__restrict__ o,
                                                            float *__restrict__ delta, float *__restrict__ lse2) {
@@ -74,8 +74,10 @@ __global__ void __launch_bounds__(256) packed_stats_kernel(const PackedArgs a, c
   for (int w = kLanes / 2; w > 0; w >>= 1) s += __shfl_xor_sync(0xffffffffu, s, w);
   if (in && sub == 0) {
     const float L = a.lse[(int64_t)h * a.qs.rows + row];
-    delta[(int64_t)h * a.qs.rows + row] = s;
-    lse2[(int64_t)h * a.qs.rows + row] = isfinite(L) ? L * kLog2e : INFINITY;
+    const int kvh = h / a.group;
+    const int64_t at = ((int64_t)kvh * a.qs.rows + row) * a.group + h - kvh * a.group;
+    delta[at] = s;
+    lse2[at] = isfinite(L) ? L * kLog2e : INFINITY;
   }
 }
 

@@ -1,0 +1,651 @@
+// Dense attention backward over packed sequences on the tcgen05 tensor cores:
+//   P = 2^(scale log2e S - LSE log2e),  dP = dO V^T,  dS = P (dP - D),
+//   dV = P^T dO,  dK = scale dS^T Q,  dQ = scale dS K.
+//
+// Two kinds of CTA, neither of which shares a sum with another, so results do
+// not depend on their order:
+//   keys     128 keys of one kv head; walks the query tiles that see them (the
+//            heads of the group are rows of the same tiles) and keeps dK and dV
+//            in tensor memory:  S^T = K Q^T, dP^T = V dO^T, dV += P^T dO,
+//            dK += dS^T Q with P^T and dS^T as operands from tensor memory
+//   queries  128 flattened query rows; walks their key tiles and keeps dQ:
+//            S = Q K^T, dP = dO V^T, dQ += dS K
+// That is 7 products for the algorithm's 5 and the exponentials twice.  The
+// other way, one kind that adds its part of dQ to an fp32 array with atomics,
+// saves two products but writes 64 KB of reductions per tile pair and gives dQ
+// whose last bits change from run to run.
+//
+// P and dS enter their products rounded once to bf16, the type of dO, Q and K
+// (a product's operands have one type); everything else is fp32.
+//
+// Warps of either kind: 0 TMA producer, 1 MMA issuer and tensor-memory owner,
+// 2-9 elementwise, a row of the tile per thread (its tensor-memory lane), warps
+// 2-5 for columns [0, 64) and 6-9 for [64, 128).  A thread writes its 16-bit
+// operand over the first 32 of its own 64 columns, so k-step k (16 rows of the
+// sum) sits at column 8k + (k >= 4 ? 32 : 0).
+#pragma once
+
+#include "packed_fwd_tc.cuh"
+
+namespace prism {
+
+constexpr int kPbThreads = 320;
+// Two resident tiles, three stages of one streamed tensor, two of the other,
+// two floats per row for two stages, barriers.  The window has no slack for
+// alignment: the kernel checks that it starts on 1024 bytes.
+template <int D>
+constexpr int kPbSmem = Tile<D>::kBytes * 7 + 2 * 1024 + 256;
+static_assert(kPbSmem<128> <= 232448, "backward shared memory");
+
+__device__ __forceinline__ uint32_t operand_col(int k) { return 8u * (uint32_t)k + (k >= 4 ? 32u : 0u); }
+
+// Waits of a whole warp: all lanes go on or none does.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int *abort, uint32_t limit) {
+  return __all_sync(0xffffffffu, tc::mbar_wait(bar, parity, abort, limit));
+}
+
+// dS = P (dP - D) over 64 columns of dP starting at `src`, packed to bf16 at `dst`
+// in chunks of 16 columns; chunk c + 1 is loaded while chunk c is computed.
+// delta(j): D of column j (a multiple of 4) .. j + 3.
+template <typename F>
+__device__ __forceinline__ void form_ds(uint32_t src, uint32_t dst, const uint32_t (&p)[64], F delta) {
+  uint32_t a[16], b[16];
+  tc::tmem_ld16(src, a);
+  tc::tmem_ld_wait_regs(a);
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    uint32_t(&cur)[16] = (c & 1) ? b : a;
+    uint32_t(&nxt)[16] = (c & 1) ? a : b;
+    if (c < 3) tc::tmem_ld16(src + 16u * (c + 1), nxt);
+    uint32_t w[8];
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+      const int j = 16 * c + 4 * g;
+      const float4 d = delta(j);
+      const float2 x = tc::mul2(tc::f2u(p[j], p[j + 1]), tc::sub2(tc::f2u(cur[4 * g], cur[4 * g + 1]), tc::f2(d.x, d.y)));
+      const float2 y = tc::mul2(tc::f2u(p[j + 2], p[j + 3]), tc::sub2(tc::f2u(cur[4 * g + 2], cur[4 * g + 3]), tc::f2(d.z, d.w)));
+      w[2 * g] = pack_bf16(x.x, x.y);
+      w[2 * g + 1] = pack_bf16(y.x, y.y);
+    }
+    if (c < 3) tc::tmem_ld_wait_regs(nxt);
+    tc::tmem_st8(dst + 8u * c, w);   // dst may be src: columns below 16 (c + 1) have been read
+  }
+}
+
+// One 64-column half of an accumulator row, times `mul`, as bf16.
+template <int COLS>
+__device__ __forceinline__ void store_row(uint32_t taddr, bool have, bool zero, float mul, __nv_bfloat16 *out) {
+#pragma unroll
+  for (int c = 0; c < COLS / 32; ++c) {
+    uint32_t v[32];
+    if (zero) {
+#pragma unroll
+      for (int e = 0; e < 32; ++e) v[e] = 0u;
+    } else {
+      tc::tmem_ld32(taddr + 32u * c, v);
+      tc::tmem_ld_wait();
+    }
+    if (have) {
+#pragma unroll
+      for (int v8 = 0; v8 < 4; ++v8) {
+        uint4 w;
+        uint32_t *wp = &w.x;
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          wp[e] = pack_bf16(__uint_as_float(v[8 * v8 + 2 * e]) * mul, __uint_as_float(v[8 * v8 + 2 * e + 1]) * mul);
+        *reinterpret_cast<uint4 *>(out + 32 * c + 8 * v8) = w;
+      }
+    }
+    __syncwarp();
+  }
+}
+
+template <int D>
+__global__ void __launch_bounds__(kPbThreads, 1)
+    packed_dkdv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                          const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmO,
+                          const PackedArgs a, const uint32_t limit) {
+  using T = Tile<D>;
+  extern __shared__ __align__(1024) uint8_t sgen[];
+  const uint32_t sbase = smem_u32(sgen);
+  if (sbase & 1023u) {
+    if (threadIdx.x == 0) set_status(PRISM_EBOUNDS);
+    return;
+  }
+  const uint32_t sK = sbase, sV = sbase + T::kBytes;
+  auto sQ = [&](int i) { return sbase + (uint32_t)(2 + i) * T::kBytes; };
+  auto sO = [&](int i) { return sbase + (uint32_t)(5 + i) * T::kBytes; };
+  auto stat = [&](int i) { return reinterpret_cast<float *>(sgen + 7 * T::kBytes + 1024 * i); };   // [lse2 | D][128]
+  const uint32_t sBar = sbase + 7 * T::kBytes + 2 * 1024;
+  auto b_qfull = [&](int i) { return sBar + 8u * i; };
+  auto b_qempty = [&](int i) { return sBar + 8u * (3 + i); };
+  auto b_ofull = [&](int i) { return sBar + 8u * (6 + i); };
+  auto b_oempty = [&](int i) { return sBar + 8u * (8 + i); };
+  const uint32_t b_kv = sBar + 8u * 10;
+  const uint32_t b_s = sBar + 8u * 11;      // S^T_n done
+  const uint32_t b_dp = sBar + 8u * 12;     // dP^T_n done
+  const uint32_t b_p = sBar + 8u * 13;      // P^T_n written
+  const uint32_t b_ds = sBar + 8u * 14;     // dS^T_n written
+  const uint32_t b_qedge = sBar + 8u * 15;  // the last tile of Q, of dO landed
+  const uint32_t b_oedge = sBar + 8u * 16;
+  const uint32_t b_drain = sBar + 8u * 17;
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sgen + (sBar - sbase) + 8 * 20);
+  volatile int *abort = reinterpret_cast<volatile int *>(sgen + (sBar - sbase) + 8 * 20 + 4);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int kvh = (int)(blockIdx.x % a.kv_heads), slot = (int)(blockIdx.x / a.kv_heads);
+  int64_t piece;
+  const int b = find_sequence(a.ks, slot, 1, 128, piece);
+  PackedSeq s;
+  if (!s.load(a, b)) return;
+  if (piece < 0 || piece * 128 >= s.room) return;
+  const int key0 = (int)piece * 128;
+  // query tiles of `tt` tokens; token t sees key j when j <= t + lk - lq (causal)
+  const int tt = 128 / a.group;
+  const int behind = a.causal ? s.lk - s.lq : 0x40000000;   // token t sees key j iff t >= j - behind
+  const int ntile = (s.lq + tt - 1) / tt;
+  const int first = key0 < s.lk ? min(ntile, max(0, key0 - behind) / tt) : ntile;
+  const int nsteps = ntile - first;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < 3; ++i) {
+      tc::mbar_init(b_qfull(i), 33);     // the copy, and each producer lane's rows of LSE and D
+      tc::mbar_init(b_qempty(i), 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      tc::mbar_init(b_ofull(i), 1);
+      tc::mbar_init(b_oempty(i), 1);
+    }
+    tc::mbar_init(b_kv, 1);
+    tc::mbar_init(b_s, 1);
+    tc::mbar_init(b_dp, 1);
+    tc::mbar_init(b_p, 256);
+    tc::mbar_init(b_ds, 256);
+    tc::mbar_init(b_qedge, 1);
+    tc::mbar_init(b_oedge, 1);
+    tc::mbar_init(b_drain, 1);
+    *abort = 0;
+    tc::fence_barrier_init();
+  }
+  if (warp == 1) {
+    tc::tmem_alloc(smem_u32(tmem_slot), 512);
+    tc::tmem_relinquish();
+  }
+  if (tt * a.group < 128 && warp >= 2 && warp < 7) {   // rows of the streamed tiles that no copy fills
+    T::zero_rows(sgen + (2 + warp - 2) * T::kBytes, tt * a.group);
+    fence_async_smem();
+  }
+  tc::tc_fence_before();
+  __syncthreads();
+  tc::tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const uint32_t tdK = tmem, tdV = tmem + 128, tS = tmem + 256, tDP = tmem + 384;
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ producer
+    int nq = 0, no = 0, qedge = 0, oedge = 0;
+    const int tile_bytes = tt * a.group * D * 2;
+    auto fetch = [&](uint32_t dst, const CUtensorMap *map, int tok, uint32_t bar) {
+      tc::mbar_expect_tx(bar, tile_bytes);
+#pragma unroll
+      for (int c = 0; c < T::kAtoms; ++c) tma_load_3d(dst + c * T::kAtom, map, 64 * c, kvh * a.group, s.q0 + tok, bar);
+    };
+    if (lane == 0 && nsteps > 0) {
+      tc::mbar_expect_tx(b_kv, 2 * T::kBytes);
+      T::load(sK, &tmK, kvh, s.k0 + key0, b_kv);
+      T::load(sV, &tmV, kvh, s.k0 + key0, b_kv);
+    }
+    const float *glse = a.lse2 + (int64_t)kvh * a.qs.rows * a.group, *gd = a.delta + (int64_t)kvh * a.qs.rows * a.group;
+    for (int n = 0; n < nsteps; ++n) {
+      const int tok = (first + n) * tt;
+      const int valid = min(tt, s.lq - tok) * a.group;     // rows of the tile
+      const bool last = s.lq - tok < tt;
+      const int qi = n % 3, oi = n & 1;
+      if (!warp_wait(b_qempty(qi), ((uint32_t)(n / 3) & 1u) ^ 1u, abort, limit)) break;
+      if (lane == 0) fetch(sQ(qi), &tmQ, tok, last ? b_qedge : b_qfull(qi));
+      (last ? qedge : nq) += 1;
+      {
+        const int64_t r = (int64_t)(s.q0 + tok) * a.group;
+        float L[4], Dr[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int c = lane + 32 * i;
+          L[i] = c < valid ? glse[r + c] : INFINITY;       // rows without a query: P = 0
+          Dr[i] = c < valid ? gd[r + c] : 0.f;
+        }
+        // dK_{n-2} follows the last use of that tile's rows of LSE and D
+        if (n >= 2 && !warp_wait(b_qempty((n - 2) % 3), (uint32_t)((n - 2) / 3) & 1u, abort, limit)) break;
+        float *st = stat(n & 1);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          st[lane + 32 * i] = L[i];
+          st[128 + lane + 32 * i] = Dr[i];
+        }
+      }
+      if (last) {
+        if (!warp_wait(b_qedge, 0, abort, limit)) break;
+        T::zero_rows(sgen + (sQ(qi) - sbase), valid);
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(b_qfull(qi));
+      }
+      tc::mbar_arrive(b_qfull(qi));
+      if (!warp_wait(b_oempty(oi), ((uint32_t)(n >> 1) & 1u) ^ 1u, abort, limit)) break;
+      if (lane == 0) fetch(sO(oi), &tmO, tok, last ? b_oedge : b_ofull(oi));
+      if (last) {
+        oedge = 1;
+        if (!warp_wait(b_oedge, 0, abort, limit)) break;
+        T::zero_rows(sgen + (sO(oi) - sbase), valid);
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(b_ofull(oi));
+      } else {
+        ++no;
+      }
+    }
+    // Every copy lands before the CTA exits (the last tile took the stage of the
+    // oldest fill, which had been read; each remaining parity is unambiguous).
+    if (lane == 0 && nsteps > 0) {
+      volatile int no_abort = 0;
+      tc::mbar_wait(b_kv, 0, &no_abort, limit);
+      for (int k = max(0, nq - 3 + qedge); k < nq; ++k)
+        tc::mbar_wait(b_qfull(k % 3), (uint32_t)(k / 3) & 1u, &no_abort, limit);
+      for (int k = max(0, no - 2 + oedge); k < no; ++k)
+        tc::mbar_wait(b_ofull(k & 1), (uint32_t)(k >> 1) & 1u, &no_abort, limit);
+      if (qedge) tc::mbar_wait(b_qedge, 0, &no_abort, limit);
+      if (oedge) tc::mbar_wait(b_oedge, 0, &no_abort, limit);
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ MMA issuer
+    if (lane == 0) {
+      constexpr uint32_t idS = tc::idesc_bf16(128, 128, false, false);
+      constexpr uint32_t idG = tc::idesc_bf16(128, D, false, true);
+      const uint64_t dK = tc::sw128_desc(sK, 16, 1024), dV = tc::sw128_desc(sV, 16, 1024);
+      auto wait = [&](uint32_t bar, uint32_t parity) {
+        const bool r = tc::mbar_wait(bar, parity, abort, limit);
+        tc::tc_fence_after();
+        return r;
+      };
+      auto rows_by_rows = [&](uint32_t d, uint64_t x, uint32_t saddr, uint32_t bar) {   // d = x y^T, both K-major
+        const uint64_t y = tc::sw128_desc(saddr, 16, 1024);
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k)
+          tc::mma_ss(d, tc::desc_adv(x, T::kstep(k)), tc::desc_adv(y, T::kstep(k)), idS, k > 0);
+        tc::mma_commit(bar);
+      };
+      auto accumulate = [&](uint32_t d, uint32_t x, uint32_t saddr, bool begun) {       // d += x y
+        const uint64_t y = tc::sw128_desc(saddr, T::kAtom, 1024);
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          tc::mma_ts(d, x + operand_col(k), tc::desc_adv(y, 2048u * k), idG, (begun || k > 0) ? 1u : 0u);
+      };
+      bool ok = nsteps > 0 && wait(b_kv, 0) && wait(b_qfull(0), 0);
+      if (ok) {
+        rows_by_rows(tS, dK, sQ(0), b_s);
+        ok = wait(b_ofull(0), 0);
+        if (ok) rows_by_rows(tDP, dV, sO(0), b_dp);
+      }
+      for (int n = 0; ok && n < nsteps; ++n) {
+        const int m = n + 1;
+        const bool more = m < nsteps;
+        if (!wait(b_p, (uint32_t)n & 1u)) break;
+        accumulate(tdV, tS, sO(n & 1), n > 0);
+        tc::mma_commit(b_oempty(n & 1));
+        if (more) {
+          if (!wait(b_qfull(m % 3), (uint32_t)(m / 3) & 1u)) break;
+          rows_by_rows(tS, dK, sQ(m % 3), b_s);
+        }
+        if (!wait(b_ds, (uint32_t)n & 1u)) break;
+        accumulate(tdK, tDP, sQ(n % 3), n > 0);
+        tc::mma_commit(b_qempty(n % 3));
+        if (more) {
+          if (!wait(b_ofull(m & 1), (uint32_t)(m >> 1) & 1u)) break;
+          rows_by_rows(tDP, dV, sO(m & 1), b_dp);
+        }
+      }
+      tc::mma_commit(b_drain);
+      volatile int no_abort = 0;
+      tc::mbar_wait(b_drain, 0, &no_abort, limit);
+    }
+  } else {
+    // ------------------------------------------------------------ elementwise
+    const int q = warp & 3, half = (warp - 2) >> 2;
+    const int row = 32 * q + lane;
+    const uint32_t lane_off = (uint32_t)(32 * q) << 16;
+    const uint32_t colS = tS + lane_off + 64u * half, colDP = tDP + lane_off + 64u * half;
+    const float cS = a.scale_log2;
+    // the tile's rows from (j - behind - token) group on see key j
+    const int64_t from0 = (int64_t)(key0 + row - behind) * a.group - 64 * half;
+    bool ok = true;
+    for (int n = 0; n < nsteps; ++n) {
+      const int qi = n % 3;
+      if (!warp_wait(b_qfull(qi), (uint32_t)(n / 3) & 1u, abort, limit) || !warp_wait(b_s, (uint32_t)n & 1u, abort, limit)) {
+        ok = false;
+        break;
+      }
+      tc::tc_fence_after();
+      const float4 *st = reinterpret_cast<const float4 *>(stat(n & 1)) + 16 * half;
+      uint32_t p[64];
+      {
+        uint32_t(&lo)[32] = *reinterpret_cast<uint32_t(*)[32]>(p);
+        uint32_t(&hi)[32] = *reinterpret_cast<uint32_t(*)[32]>(p + 32);
+        tc::tmem_ld32(colS, lo);
+        tc::tmem_ld32(colS + 32u, hi);
+        tc::tmem_ld_wait();
+      }
+      // first column of this half that sees the key
+      const int from = (int)max((int64_t)0, min((int64_t)64, from0 - (int64_t)(first + n) * tt * a.group));
+      const bool mask = __any_sync(0xffffffffu, from > 0);
+#pragma unroll
+      for (int j = 0; j < 64; j += 4) {
+        const float4 L = st[j / 4];
+        float2 x = tc::fma2(tc::f2u(p[j], p[j + 1]), tc::f2(cS, cS), tc::f2(-L.x, -L.y));
+        float2 y = tc::fma2(tc::f2u(p[j + 2], p[j + 3]), tc::f2(cS, cS), tc::f2(-L.z, -L.w));
+        if (mask) {
+          if (j + 0 < from) x.x = -INFINITY;
+          if (j + 1 < from) x.y = -INFINITY;
+          if (j + 2 < from) y.x = -INFINITY;
+          if (j + 3 < from) y.y = -INFINITY;
+        }
+        p[j] = __float_as_uint(tc::ex2(x.x));
+        p[j + 1] = __float_as_uint(tc::ex2(x.y));
+        p[j + 2] = __float_as_uint(tc::ex2(y.x));
+        p[j + 3] = __float_as_uint(tc::ex2(y.y));
+      }
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        uint32_t w[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+          w[e] = pack_bf16(__uint_as_float(p[32 * c + 2 * e]), __uint_as_float(p[32 * c + 2 * e + 1]));
+        tc::tmem_st16(colS + 16u * c, w);
+      }
+      tc::tmem_st_wait();
+      tc::tc_fence_before();
+      tc::mbar_arrive(b_p);
+      if (!warp_wait(b_dp, (uint32_t)n & 1u, abort, limit)) {
+        ok = false;
+        break;
+      }
+      tc::tc_fence_after();
+      form_ds(colDP, colDP, p, [&](int j) { return st[32 + j / 4]; });
+      tc::tmem_st_wait();
+      tc::tc_fence_before();
+      tc::mbar_arrive(b_ds);
+    }
+    if (__all_sync(0xffffffffu, ok && !*abort)) {
+      if (nsteps > 0) ok = warp_wait(b_drain, 0, abort, limit);
+      if (ok) {
+        tc::tc_fence_after();
+        const int key = key0 + row;
+        const bool have = key < s.room;
+        const bool zero = nsteps == 0;
+        const float keep = key < s.lk ? 1.f : 0.f;    // rows with room but not in use: zero
+        const int64_t r = s.k0 + key;
+        constexpr int kCols = D / 2;                  // of each half's warps
+        const uint32_t co = lane_off + (uint32_t)(half * kCols);
+        __nv_bfloat16 *dk = a.dk + r * a.sdk[0] + kvh * a.sdk[1] + half * kCols;
+        __nv_bfloat16 *dv = a.dv + r * a.sdv[0] + kvh * a.sdv[1] + half * kCols;
+        if (__any_sync(0xffffffffu, have && keep == 0.f && !zero)) {
+          // a tile with rows behind the keys in use: those rows are zeros, whatever their accumulators hold
+          store_row<kCols>(tdK + co, have && keep != 0.f, zero, a.scale, dk);
+          store_row<kCols>(tdV + co, have && keep != 0.f, zero, 1.f, dv);
+          store_row<kCols>(tdK + co, have && keep == 0.f, true, 0.f, dk);
+          store_row<kCols>(tdV + co, have && keep == 0.f, true, 0.f, dv);
+        } else {
+          store_row<kCols>(tdK + co, have, zero, a.scale, dk);
+          store_row<kCols>(tdV + co, have, zero, 1.f, dv);
+        }
+      }
+    }
+  }
+  tc::tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc::tc_fence_after();
+    tc::tmem_dealloc(tmem, 512);
+  }
+}
+
+template <int D>
+__global__ void __launch_bounds__(kPbThreads, 1)
+    packed_dq_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                        const PackedArgs a, const uint32_t limit) {
+  using T = Tile<D>;
+  extern __shared__ __align__(1024) uint8_t sgen[];
+  const uint32_t sbase = smem_u32(sgen);
+  if (sbase & 1023u) {
+    if (threadIdx.x == 0) set_status(PRISM_EBOUNDS);
+    return;
+  }
+  const uint32_t sQ = sbase, sO = sbase + T::kBytes;
+  auto sK = [&](int i) { return sbase + (uint32_t)(2 + i) * T::kBytes; };
+  auto sV = [&](int i) { return sbase + (uint32_t)(5 + i) * T::kBytes; };
+  const uint32_t sBar = sbase + 7 * T::kBytes + 2 * 1024;
+  auto b_kfull = [&](int i) { return sBar + 8u * i; };
+  auto b_kempty = [&](int i) { return sBar + 8u * (3 + i); };
+  auto b_vfull = [&](int i) { return sBar + 8u * (6 + i); };
+  auto b_vempty = [&](int i) { return sBar + 8u * (8 + i); };
+  auto b_s = [&](int i) { return sBar + 8u * (10 + i); };     // S_n done
+  const uint32_t b_dp = sBar + 8u * 12;     // dP_n done
+  const uint32_t b_ds = sBar + 8u * 13;     // dS_n written
+  const uint32_t b_kedge = sBar + 8u * 14;  // the last tile of K, of V landed
+  const uint32_t b_vedge = sBar + 8u * 15;
+  const uint32_t b_drain = sBar + 8u * 16;
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sgen + (sBar - sbase) + 8 * 20);
+  volatile int *abort = reinterpret_cast<volatile int *>(sgen + (sBar - sbase) + 8 * 20 + 4);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int slots = (int)(gridDim.x / a.kv_heads);
+  const int kvh = (int)(blockIdx.x % a.kv_heads), slot = slots - 1 - (int)(blockIdx.x / a.kv_heads);
+  PackedSeq::check(a, slot);
+  int64_t piece;
+  const int b = find_sequence(a.qs, slot, a.group, 128, piece);
+  PackedSeq s;
+  if (!s.load(a, b)) return;
+  const int64_t nrows = (int64_t)s.lq * a.group;
+  if (piece < 0 || piece * 128 >= nrows) return;
+  const int r0 = (int)(piece * 128);
+  const int rows = (int)min((int64_t)128, nrows - r0);
+  const int nsteps = (s.visible(a, (r0 + rows - 1) / a.group) + 127) >> 7;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < 3; ++i) {
+      tc::mbar_init(b_kfull(i), 1);
+      tc::mbar_init(b_kempty(i), 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      tc::mbar_init(b_vfull(i), 1);
+      tc::mbar_init(b_vempty(i), 1);
+      tc::mbar_init(b_s(i), 1);
+    }
+    tc::mbar_init(b_dp, 1);
+    tc::mbar_init(b_ds, 256);
+    tc::mbar_init(b_kedge, 1);
+    tc::mbar_init(b_vedge, 1);
+    tc::mbar_init(b_drain, 1);
+    *abort = 0;
+    tc::fence_barrier_init();
+  }
+  if (warp == 1) {
+    tc::tmem_alloc(smem_u32(tmem_slot), 512);
+    tc::tmem_relinquish();
+  }
+  for (int i = threadIdx.x; i < 128 * (D / 8); i += kPbThreads) {
+    const int r = i / (D / 8), ch = i % (D / 8);
+    const bool have = r < rows;
+    const int fr = r0 + (have ? r : 0), tok = fr / a.group, head = kvh * a.group + fr - tok * a.group;
+    cp_async16_or_zero(sQ + T::off(r, ch), a.q + (int64_t)(s.q0 + tok) * a.sq[0] + (int64_t)head * a.sq[1] + ch * 8, have);
+    cp_async16_or_zero(sO + T::off(r, ch), a.dout + (int64_t)(s.q0 + tok) * a.sdo[0] + (int64_t)head * a.sdo[1] + ch * 8, have);
+  }
+  cp_async_commit();
+  cp_async_wait<0>();
+  fence_async_smem();
+  tc::tc_fence_before();
+  __syncthreads();
+  tc::tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  auto tS = [&](int i) { return tmem + 128u * (uint32_t)i; };
+  const uint32_t tDP = tmem + 256, tdQ = tmem + 384;
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ producer
+    int nk = 0, nv = 0, kedge = 0, vedge = 0;
+    for (int n = 0; n < nsteps; ++n) {
+      const int valid = s.lk - 128 * n, ki = n % 3, vi = n & 1;
+      const bool last = valid < 128;
+      if (!warp_wait(b_kempty(ki), ((uint32_t)(n / 3) & 1u) ^ 1u, abort, limit)) break;
+      if (lane == 0) {
+        const uint32_t bar = last ? b_kedge : b_kfull(ki);
+        tc::mbar_expect_tx(bar, T::kBytes);
+        T::load(sK(ki), &tmK, kvh, s.k0 + 128 * n, bar);
+      }
+      if (last) {   // other rows' keys would meet dS = 0 in the product for dQ: they must be numbers
+        kedge = 1;
+        if (!warp_wait(b_kedge, 0, abort, limit)) break;
+        T::zero_rows(sgen + (sK(ki) - sbase), valid);
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(b_kfull(ki));
+      } else {
+        ++nk;
+      }
+      if (!warp_wait(b_vempty(vi), ((uint32_t)(n >> 1) & 1u) ^ 1u, abort, limit)) break;
+      if (lane == 0) {
+        const uint32_t bar = last ? b_vedge : b_vfull(vi);
+        tc::mbar_expect_tx(bar, T::kBytes);
+        T::load(sV(vi), &tmV, kvh, s.k0 + 128 * n, bar);
+      }
+      if (last) {
+        vedge = 1;
+        if (!warp_wait(b_vedge, 0, abort, limit)) break;
+        T::zero_rows(sgen + (sV(vi) - sbase), valid);
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(b_vfull(vi));
+      } else {
+        ++nv;
+      }
+    }
+    if (lane == 0) {
+      volatile int no_abort = 0;
+      for (int k = max(0, nk - 3 + kedge); k < nk; ++k)
+        tc::mbar_wait(b_kfull(k % 3), (uint32_t)(k / 3) & 1u, &no_abort, limit);
+      for (int k = max(0, nv - 2 + vedge); k < nv; ++k)
+        tc::mbar_wait(b_vfull(k & 1), (uint32_t)(k >> 1) & 1u, &no_abort, limit);
+      if (kedge) tc::mbar_wait(b_kedge, 0, &no_abort, limit);
+      if (vedge) tc::mbar_wait(b_vedge, 0, &no_abort, limit);
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ MMA issuer
+    if (lane == 0 && nsteps > 0) {
+      constexpr uint32_t idS = tc::idesc_bf16(128, 128, false, false);
+      constexpr uint32_t idG = tc::idesc_bf16(128, D, false, true);
+      const uint64_t dQ = tc::sw128_desc(sQ, 16, 1024), dO = tc::sw128_desc(sO, 16, 1024);
+      auto wait = [&](uint32_t bar, uint32_t parity) {
+        const bool r = tc::mbar_wait(bar, parity, abort, limit);
+        tc::tc_fence_after();
+        return r;
+      };
+      auto rows_by_rows = [&](uint32_t d, uint64_t x, uint32_t saddr, uint32_t bar) {
+        const uint64_t y = tc::sw128_desc(saddr, 16, 1024);
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k)
+          tc::mma_ss(d, tc::desc_adv(x, T::kstep(k)), tc::desc_adv(y, T::kstep(k)), idS, k > 0);
+        tc::mma_commit(bar);
+      };
+      auto scores = [&](int n) {
+        if (!wait(b_kfull(n % 3), (uint32_t)(n / 3) & 1u)) return false;
+        rows_by_rows(tS(n & 1), dQ, sK(n % 3), b_s(n & 1));
+        return true;
+      };
+      auto dprob = [&](int n) {
+        if (!wait(b_vfull(n & 1), (uint32_t)(n >> 1) & 1u)) return false;
+        rows_by_rows(tDP, dO, sV(n & 1), b_dp);
+        tc::mma_commit(b_vempty(n & 1));
+        return true;
+      };
+      bool ok = scores(0) && dprob(0) && (nsteps < 2 || scores(1));
+      for (int n = 0; ok && n < nsteps; ++n) {
+        if (!wait(b_ds, (uint32_t)n & 1u)) break;
+        if (n + 1 < nsteps && !dprob(n + 1)) break;
+        const uint64_t y = tc::sw128_desc(sK(n % 3), T::kAtom, 1024);
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          tc::mma_ts(tdQ, tS(n & 1) + operand_col(k), tc::desc_adv(y, 2048u * k), idG, (n > 0 || k > 0) ? 1u : 0u);
+        tc::mma_commit(b_kempty(n % 3));
+        if (n + 2 < nsteps && !scores(n + 2)) break;
+      }
+      tc::mma_commit(b_drain);
+      volatile int no_abort = 0;
+      tc::mbar_wait(b_drain, 0, &no_abort, limit);
+    }
+  } else {
+    // ------------------------------------------------------------ elementwise
+    const int q = warp & 3, half = (warp - 2) >> 2;
+    const int row = 32 * q + lane;
+    const uint32_t lane_off = (uint32_t)(32 * q) << 16;
+    const bool have = row < rows;
+    const int fr = r0 + row, tok = have ? fr / a.group : 0, head = kvh * a.group + fr - tok * a.group;
+    const int vis = have ? s.visible(a, tok) : 0;
+    const int64_t st = (int64_t)kvh * a.qs.rows * a.group + (int64_t)s.q0 * a.group + fr;
+    const float nl = have ? -a.lse2[st] : -INFINITY, delta = have ? a.delta[st] : 0.f;
+    const float4 d4 = make_float4(delta, delta, delta, delta);
+    const float cS = a.scale_log2;
+    bool ok = true;
+    for (int n = 0; n < nsteps; ++n) {
+      if (!warp_wait(b_s(n & 1), (uint32_t)(n >> 1) & 1u, abort, limit)) {
+        ok = false;
+        break;
+      }
+      tc::tc_fence_after();
+      const uint32_t colS = tS(n & 1) + lane_off + 64u * half;
+      uint32_t p[64];
+      {
+        uint32_t(&lo)[32] = *reinterpret_cast<uint32_t(*)[32]>(p);
+        uint32_t(&hi)[32] = *reinterpret_cast<uint32_t(*)[32]>(p + 32);
+        tc::tmem_ld32(colS, lo);
+        tc::tmem_ld32(colS + 32u, hi);
+        tc::tmem_ld_wait();
+      }
+      const int seen = vis - 128 * n - 64 * half;
+      const bool mask = __any_sync(0xffffffffu, seen < 64);
+#pragma unroll
+      for (int j = 0; j < 64; j += 2) {
+        float2 x = tc::fma2(tc::f2u(p[j], p[j + 1]), tc::f2(cS, cS), tc::f2(nl, nl));
+        if (mask) {
+          if (j + 0 >= seen) x.x = -INFINITY;
+          if (j + 1 >= seen) x.y = -INFINITY;
+        }
+        p[j] = __float_as_uint(tc::ex2(x.x));
+        p[j + 1] = __float_as_uint(tc::ex2(x.y));
+      }
+      if (!warp_wait(b_dp, (uint32_t)n & 1u, abort, limit)) {
+        ok = false;
+        break;
+      }
+      tc::tc_fence_after();
+      form_ds(tDP + lane_off + 64u * half, colS, p, [&](int) { return d4; });
+      tc::tmem_st_wait();
+      tc::tc_fence_before();
+      tc::mbar_arrive(b_ds);
+    }
+    if (__all_sync(0xffffffffu, ok && !*abort)) {
+      if (nsteps > 0) ok = warp_wait(b_drain, 0, abort, limit);
+      if (ok) {
+        tc::tc_fence_after();
+        constexpr int kCols = D / 2;
+        store_row<kCols>(tdQ + lane_off + (uint32_t)(half * kCols), have, nsteps == 0, a.scale,
+                         a.dq + (int64_t)(s.q0 + tok) * a.sdq[0] + (int64_t)head * a.sdq[1] + half * kCols);
+      }
+    }
+  }
+  tc::tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc::tc_fence_after();
+    tc::tmem_dealloc(tmem, 512);
+  }
+}
+
+}  // namespace prism

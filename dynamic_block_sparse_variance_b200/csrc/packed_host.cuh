@@ -3,8 +3,7 @@
 #pragma once
 
 #include "block_norm.cuh"
-#include "packed_fwd_tc.cuh"
-#include "packed_simple.cuh"
+#include "packed_bwd_tc.cuh"
 
 namespace prism {
 
@@ -143,15 +142,31 @@ static int launch_packed_fwd(const prism_packed_params *p, const PackedArgs &a, 
 template <int D>
 static int launch_packed_bwd(const prism_packed_params *p, const PackedArgs &a, float *delta, float *lse2,
                              cudaStream_t st) {
-  if (p->q_rows) {
-    const int64_t threads = (int64_t)p->q_rows * p->heads * (D / 4);
+  const int64_t dummy[2] = {D, D};
+  const bool keys = p->k_rows > 0, rows = p->q_rows > 0;
+  const int tt = 128 / a.group;     // tokens per streamed query tile
+  const void *any = rows ? (const void *)a.q : a.k;
+  CUtensorMap tq, to, tk, tv;
+  if (!make_head_map(&tk, keys ? (const void *)a.k : any, D, keys ? a.kv_heads : 1, keys ? p->k_rows : 1, keys ? a.sk : dummy) ||
+      !make_head_map(&tv, keys ? (const void *)a.v : any, D, keys ? a.kv_heads : 1, keys ? p->k_rows : 1, keys ? a.sv : dummy) ||
+      !make_head_map(&tq, any, D, rows ? a.heads : 1, rows ? p->q_rows : 1, rows ? a.sq : dummy, a.group, tt) ||
+      !make_head_map(&to, rows ? (const void *)a.dout : any, D, rows ? a.heads : 1, rows ? p->q_rows : 1, rows ? a.sdo : dummy, a.group, tt))
+    return fail(PRISM_ECUDA, "cuTensorMapEncodeTiled failed");
+  if (rows) {
+    const int64_t threads = p->q_rows * p->heads * (D / 4);
     PRISM_TRACED("packed_stats_kernel", st, packed_stats_kernel<D><<<(unsigned)((threads + 255) / 256), 256, 0, st>>>(a, a.o, delta, lse2));
-    const dim3 qgrid((unsigned)slot_bound(p->q_rows, p->seqs, a.group, 8), a.kv_heads);
-    PRISM_TRACED("packed_dq_simple_kernel", st, packed_dq_simple_kernel<D><<<qgrid, 256, 0, st>>>(a));
   }
-  if (p->k_rows) {
-    const dim3 kgrid((unsigned)slot_bound(p->k_rows, p->seqs, 1, 8), a.kv_heads);
-    PRISM_TRACED("packed_dkdv_simple_kernel", st, packed_dkdv_simple_kernel<D><<<kgrid, 256, 0, st>>>(a));
+  if (keys) {
+    const int64_t grid = slot_bound(p->k_rows, p->seqs, 1, 128) * a.kv_heads;
+    if (grid > 0x7fffffffLL) return fail(PRISM_EINVAL, "packed: too many key rows");
+    cudaFuncSetAttribute(packed_dkdv_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, kPbSmem<D>);
+    PRISM_TRACED("packed_dkdv_tc_kernel", st, packed_dkdv_tc_kernel<D><<<(unsigned)grid, kPbThreads, kPbSmem<D>, st>>>(tq, tk, tv, to, a, wait_limit()));
+  }
+  if (rows) {
+    const int64_t grid = slot_bound(p->q_rows, p->seqs, a.group, 128) * a.kv_heads;
+    if (grid > 0x7fffffffLL) return fail(PRISM_EINVAL, "packed: too many query rows");
+    cudaFuncSetAttribute(packed_dq_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, kPbSmem<D>);
+    PRISM_TRACED("packed_dq_tc_kernel", st, packed_dq_tc_kernel<D><<<(unsigned)grid, kPbThreads, kPbSmem<D>, st>>>(tk, tv, a, wait_limit()));
   }
   return PRISM_OK;
 }

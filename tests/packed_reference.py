@@ -12,7 +12,7 @@ def offsets(lens):
 
 
 def attention(q, k, v, q_off, k_off, causal, scale, used=None, dout=None):
-    """o, lse and, with dout, dq, dk, dv; and bounds of their errors, elementwise.
+    """o, lse and, with dout, dq, dk, dv; and bounds of their errors, elementwise (with dout: a third dict).
 
     Bounds, with p the probabilities, a = p |v| and D the row sum of dout o:
       o    the probabilities enter the product with v rounded once (U a), the result is rounded once (U |o|)
@@ -21,12 +21,14 @@ def attention(q, k, v, q_off, k_off, causal, scale, used=None, dout=None):
            as an operand: U |ds| + p |dD|; dq and dk sum that times |k| or |q| and are rounded once
     Sums in 32 bits, exponentials and the 16-bit residual of o add relative errors near 2^-16: covered by a
     factor of 1.1 and by `slack` = 2^-14 of the same sums of magnitudes.
+    The part of the bounds that is such sums alone comes third: dP and D sum 128 products each, so dS is off by up to
+    2 x 128 x 2^-24 = 2^-16 of p (|dout| |v| + |dout| a) however small it is (exactly 0 where a row sees one key).
     """
     hq, hk = q.shape[1], k.shape[1]
     o, lse = np.zeros_like(q), np.full((hq, q.shape[0]), -np.inf)
     bo = np.zeros_like(q)
     g = dict(dq=np.zeros_like(q), dk=np.zeros_like(k), dv=np.zeros_like(v))
-    bg = {n: np.zeros_like(x) for n, x in g.items()}
+    bg, rest = ({n: np.zeros_like(x) for n, x in g.items()} for _ in range(2))
     slack = 2.0 ** -14
     for b in range(len(q_off) - 1):
         q0, lq = q_off[b], q_off[b + 1] - q_off[b]
@@ -62,6 +64,8 @@ def attention(q, k, v, q_off, k_off, causal, scale, used=None, dout=None):
             g["dq"][q0:q0 + lq, h] = scale * ds @ K
             g["dk"][k0:k0 + lk, j] += scale * ds.T @ Q
             g["dv"][k0:k0 + lk, j] += p.T @ G
+            rest["dq"][q0:q0 + lq, h] = scale * 2.0 ** -16 * (p * mag) @ np.abs(K)
+            rest["dk"][k0:k0 + lk, j] += scale * 2.0 ** -16 * (p * mag).T @ np.abs(Q)
             bg["dq"][q0:q0 + lq, h] = scale * eds @ np.abs(K)
             bg["dk"][k0:k0 + lk, j] += scale * eds.T @ np.abs(Q)
             bg["dv"][k0:k0 + lk, j] += (1.1 * U + slack) * p.T @ np.abs(G)
@@ -72,7 +76,7 @@ def attention(q, k, v, q_off, k_off, causal, scale, used=None, dout=None):
     if dout is not None:
         out.update(g)
         bounds.update({n: x + TINY for n, x in bg.items()})
-    return out, bounds
+    return (out, bounds) if dout is None else (out, bounds, rest)
 
 
 def _normed(z, kind, eps):

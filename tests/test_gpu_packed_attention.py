@@ -35,17 +35,18 @@ def _within(got, want, bound, what):
     assert over.size == 0 or over.max() <= 0, f"{what}: {over.max():.3e} over the bound at {int((over > 0).sum())} of {over.size} places"
 
 
-def _close_on_average(got, want, what):
-    """Independent roundings (operand, D, result) have a mean square of at most U^2 / 3 each."""
+def _close_on_average(got, want, what, rest=0.0):
+    """Independent roundings (operand, D, result) have a mean square of at most U^2 / 3 each; `rest`: what sums
+    in 32 bits may add where terms cancel (tests/packed_reference.py)."""
     got = _f64(got)
     fin = np.isfinite(want)
     norm = np.linalg.norm(want[fin])
-    assert np.linalg.norm(got[fin] - want[fin]) <= np.sqrt(3 * ref.U ** 2 / 3) * norm + 1e-30, what
+    assert np.linalg.norm(got[fin] - want[fin]) <= np.sqrt(3 * ref.U ** 2 / 3) * norm + np.linalg.norm(rest) + 1e-30, what
 
 
 def _check(q, k, v, dout, qo, ko, causal, scale, used, att, o, grads=None, what="", average=False):
-    want, bound = ref.attention(_f64(q), _f64(k), _f64(v), qo, ko, causal, scale or q.shape[-1] ** -0.5, used,
-                                _f64(dout) if grads else None)
+    want, bound, *rest = ref.attention(_f64(q), _f64(k), _f64(v), qo, ko, causal, scale or q.shape[-1] ** -0.5, used,
+                                       _f64(dout) if grads else None)
     rows = np.zeros(q.shape[0], bool)
     for a, b in zip(qo[:-1], qo[1:]):
         rows[a:b] = True
@@ -56,7 +57,7 @@ def _check(q, k, v, dout, qo, ko, causal, scale, used, att, o, grads=None, what=
             off = qo if n == "dq" else ko
             _within(g[off[0]:off[-1]], want[n][off[0]:off[-1]], bound[n][off[0]:off[-1]], what + " " + n)
             if average:
-                _close_on_average(g[off[0]:off[-1]], want[n][off[0]:off[-1]], what + " " + n)
+                _close_on_average(g[off[0]:off[-1]], want[n][off[0]:off[-1]], what + " " + n, rest[0][n])
     if average:
         _close_on_average(o[torch.from_numpy(rows).cuda()], want["o"][rows], what + " o")
 
@@ -345,7 +346,7 @@ def test_gradients_against_differences():
     att.forward(*t[:3], _ints(qo))
     grads = att.backward(t[3])
     q, k, v, do = (_f64(x) for x in t)
-    _, bound = ref.attention(q, k, v, qo, ko, True, 0.125, dout=do)
+    _, bound, _ = ref.attention(q, k, v, qo, ko, True, 0.125, dout=do)
     loss = lambda *a: float((ref.attention(*a, qo, ko, True, 0.125)[0]["o"] * do).sum())
     rng = np.random.default_rng(0)
     for i, n in enumerate(("dq", "dk", "dv")):

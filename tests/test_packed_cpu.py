@@ -43,7 +43,7 @@ def test_attention_reference_gradients_against_differences(causal):
     qo, ko = ref.offsets([3, 0, 5]), ref.offsets([4, 2, 3])
     q, k, v = rng.normal(size=(8, 4, 6)), rng.normal(size=(9, 2, 6)), rng.normal(size=(9, 2, 6))
     do = rng.normal(size=q.shape)
-    out, _ = ref.attention(q, k, v, qo, ko, causal, 0.4, dout=do)
+    out, _, _ = ref.attention(q, k, v, qo, ko, causal, 0.4, dout=do)
     loss = lambda q, k, v: float((ref.attention(q, k, v, qo, ko, causal, 0.4)[0]["o"] * do).sum())
     eps = 1e-5
     for i, n in enumerate(("dq", "dk", "dv")):
