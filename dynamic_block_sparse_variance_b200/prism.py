@@ -225,22 +225,30 @@ def prism_bsa_bwd(p, blocks, zone_blk_base, nblk, q, k, v, o, o_res, dout, lse, 
                                _ptr(workspace), workspace.numel(), _stream()))
 
 
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
 def prism_packed_workspace_size(p, kind):
     n = ctypes.c_size_t(0)
     _check(lib().prism_packed_workspace_size(ctypes.byref(p), kind, ctypes.byref(n)))
     return n.value
 
 
-def prism_packed_attn_fwd(p, q, k, v, q_off, k_off, k_used, o, o_res, lse, workspace=None):
-    _check(lib().prism_packed_attn_fwd(ctypes.byref(p), _ptr(q), _ptr(k), _ptr(v), _ptr(q_off), _ptr(k_off),
-                                       _ptr(k_used), _ptr(o), _ptr(o_res), _ptr(lse), _ptr(workspace),
-                                       0 if workspace is None else workspace.numel(), _stream()))
+def prism_packed_attn_fwd(p, q, k, v, q_off, k_off, k_used, o, o_res, lse, workspace=None, stream=None):
+    _check(lib().prism_packed_attn_fwd(ctypes.byref(p), _addr(q), _addr(k), _addr(v), _addr(q_off), _addr(k_off),
+                                       _addr(k_used), _addr(o), _addr(o_res), _addr(lse), _addr(workspace),
+                                       0 if workspace is None else workspace.numel(),
+                                       _stream() if stream is None else stream))
 
 
-def prism_packed_attn_bwd(p, q, k, v, o, o_res, dout, lse, q_off, k_off, k_used, dq, dk, dv, workspace=None):
-    _check(lib().prism_packed_attn_bwd(ctypes.byref(p), _ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(o_res), _ptr(dout),
-                                       _ptr(lse), _ptr(q_off), _ptr(k_off), _ptr(k_used), _ptr(dq), _ptr(dk), _ptr(dv),
-                                       _ptr(workspace), 0 if workspace is None else workspace.numel(), _stream()))
+def prism_packed_attn_bwd(p, q, k, v, o, o_res, dout, lse, q_off, k_off, k_used, dq, dk, dv, workspace=None,
+                          stream=None):
+    _check(lib().prism_packed_attn_bwd(ctypes.byref(p), _addr(q), _addr(k), _addr(v), _addr(o), _addr(o_res),
+                                       _addr(dout), _addr(lse), _addr(q_off), _addr(k_off), _addr(k_used), _addr(dq),
+                                       _addr(dk), _addr(dv), _addr(workspace),
+                                       0 if workspace is None else workspace.numel(),
+                                       _stream() if stream is None else stream))
 
 
 def prism_block_norm_workspace_size(p):
@@ -249,18 +257,19 @@ def prism_block_norm_workspace_size(p):
     return n.value
 
 
-def prism_block_norm_fwd(p, x, y, off, post_weight, gate, weight, scale, shift, x_out, h, y_norms=None):
-    _check(lib().prism_block_norm_fwd(ctypes.byref(p), _ptr(x), _ptr(y), _ptr(off), _ptr(post_weight), _ptr(gate),
-                                      _ptr(weight), _ptr(scale), _ptr(shift), _ptr(x_out), _ptr(h), _ptr(y_norms),
-                                      _stream()))
+def prism_block_norm_fwd(p, x, y, off, post_weight, gate, weight, scale, shift, x_out, h, y_norms=None, stream=None):
+    _check(lib().prism_block_norm_fwd(ctypes.byref(p), _addr(x), _addr(y), _addr(off), _addr(post_weight), _addr(gate),
+                                      _addr(weight), _addr(scale), _addr(shift), _addr(x_out), _addr(h), _addr(y_norms),
+                                      _stream() if stream is None else stream))
 
 
 def prism_block_norm_bwd(p, x_out, y, off, post_weight, gate, weight, scale, dh, dx_out, dx, dy, dpost_weight, dgate,
-                         dweight, dscale, dshift, workspace):
-    _check(lib().prism_block_norm_bwd(ctypes.byref(p), _ptr(x_out), _ptr(y), _ptr(off), _ptr(post_weight), _ptr(gate),
-                                      _ptr(weight), _ptr(scale), _ptr(dh), _ptr(dx_out), _ptr(dx), _ptr(dy),
-                                      _ptr(dpost_weight), _ptr(dgate), _ptr(dweight), _ptr(dscale), _ptr(dshift),
-                                      _ptr(workspace), workspace.numel(), _stream()))
+                         dweight, dscale, dshift, workspace, stream=None):
+    _check(lib().prism_block_norm_bwd(ctypes.byref(p), _addr(x_out), _addr(y), _addr(off), _addr(post_weight),
+                                      _addr(gate), _addr(weight), _addr(scale), _addr(dh), _addr(dx_out), _addr(dx),
+                                      _addr(dy), _addr(dpost_weight), _addr(dgate), _addr(dweight), _addr(dscale),
+                                      _addr(dshift), _addr(workspace), workspace.numel(),
+                                      _stream() if stream is None else stream))
 
 
 def prism_set_option(option, value):

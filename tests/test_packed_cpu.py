@@ -199,7 +199,7 @@ def test_python_layer_refuses_host_tensors_and_wrong_use():
 def test_strided_views_are_read_as_they_lie(shape, strides, heads, want):
     t = torch.zeros(4096, dtype=torch.bfloat16)
     t = t[: int(np.prod(shape))].view(shape) if strides is None else t.as_strided(shape, strides)
-    assert packed._heads_view(t, heads, 64, t.device, "t") == want
+    assert packed._heads_view(t.shape, t.stride(), heads, 64, "t") == want
 
 
 @pytest.mark.parametrize("shape,strides,heads", [
@@ -208,4 +208,4 @@ def test_strided_views_are_read_as_they_lie(shape, strides, heads, want):
 def test_unreadable_views_are_refused(shape, strides, heads):
     t = torch.zeros(8192, dtype=torch.bfloat16).as_strided(shape, strides)
     with pytest.raises(P.PrismError):
-        packed._heads_view(t, heads, 64, t.device, "t")
+        packed._heads_view(t.shape, t.stride(), heads, 64, "t")
