@@ -5,22 +5,32 @@
 // N is the identity, x / sqrt(mean(x^2) + eps), or that of x - mean(x); gate,
 // scale and shift belong to the packed sequence of the row.
 //
-// Both directions are bound by HBM: a row is read once, kept in registers
-// while its statistics are reduced, and written once.  A thread owns the same
-// 8 (or 16) columns of every row of its CTA's run of rows, so the column
-// parameters, folded to w (1 + scale), shift and gate w_post in fp32, stay in
-// registers too, and so do the backward's column sums, which leave the CTA
-// once per run.
+// Both directions are bound by HBM: a row is read once and written once.  A
+// CTA works through a run of rows of one sequence.  The rows come in through
+// bulk copies into a ring in shared memory, issued ahead by one thread, so the
+// bytes in flight do not depend on registers.  What sets the time otherwise is
+// the reductions: with a row spread over a whole CTA (8 columns a thread) every
+// statistic is a butterfly, a barrier and a table, about 1000 cycles of
+// dependent latency, and most instructions (61440 x 1536 forward: 208 us).  So
+//   forward   a row belongs to one warp (2 to 4 beyond 2048 channels), which
+//             keeps it in registers; warps run on their own, without barriers
+//   backward  the column sums, three per column, want to stay in registers, so
+//             a row is spread over the CTA all the same, two rows at a time
+// (The backward with rows by warps for the statistics and columns by threads for
+// the results reads each row three times and was slower: 331 us against 233 at
+// 30011 x 2048.)
 #pragma once
 
-#include <type_traits>
-
 #include "packed_common.cuh"
+#include "tc_common.cuh"
 
 namespace prism {
 
 constexpr int kBnMaxChannels = 8192;
-constexpr int kBnMaxThreads = 512;
+constexpr int kBnWarps = 16;          // forward
+constexpr int kBnMaxThreads = 512;    // backward
+constexpr int kBnMaxGroups = 8;       // rows of a CTA at a time, backward
+constexpr int kBnMaxStages = 4;
 
 struct BlockNormArgs {
   Offsets seq;
@@ -33,454 +43,724 @@ struct BlockNormArgs {
   int64_t sgate, sscale, sshift;                  // elements from one sequence to the next
   void *x_out, *h, *dx, *dy;
   float *y_norms;
-  float *part;               // backward: [slots * rows per pass][3][C] column sums
+  float *part;               // backward: [slots * groups][3][C] column sums
+  int need;                  // backward: bit k, column sum k is wanted
+  int wpr, groups, stages;   // warps per row, row groups of a CTA, stages of a ring
+  int vecs;                  // forward: 256-column vectors per warp
+  uint32_t wait_limit;
 };
 
-// Eight consecutive elements as loaded, and as fp32.
+// Eight consecutive elements as four fp32 pairs: sums and products run on
+// register pairs (tc::fma2 and its kin), two lanes an instruction.
 template <typename T>
 struct BnVec8;
 template <>
 struct BnVec8<__nv_bfloat16> {
-  uint4 a;
-  __device__ __forceinline__ void load(const __nv_bfloat16 *p) { a = __ldcs(reinterpret_cast<const uint4 *>(p)); }
-  __device__ __forceinline__ void get(float *f) const {
-    f[0] = bf16_lo(a.x); f[1] = bf16_hi(a.x); f[2] = bf16_lo(a.y); f[3] = bf16_hi(a.y);
-    f[4] = bf16_lo(a.z); f[5] = bf16_hi(a.z); f[6] = bf16_lo(a.w); f[7] = bf16_hi(a.w);
+  __device__ __forceinline__ static void unpack(const uint4 &a, float2 *f) {
+    f[0] = tc::f2(bf16_lo(a.x), bf16_hi(a.x));
+    f[1] = tc::f2(bf16_lo(a.y), bf16_hi(a.y));
+    f[2] = tc::f2(bf16_lo(a.z), bf16_hi(a.z));
+    f[3] = tc::f2(bf16_lo(a.w), bf16_hi(a.w));
   }
-  __device__ __forceinline__ static void store(__nv_bfloat16 *p, const float *f) {
-    __stcs(reinterpret_cast<uint4 *>(p), make_uint4(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]),
-                                                    pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7])));
+  __device__ __forceinline__ static void load(const __nv_bfloat16 *p, float2 *f) {
+    unpack(*reinterpret_cast<const uint4 *>(p), f);
+  }
+  __device__ __forceinline__ static void store(__nv_bfloat16 *p, const float2 *f) {
+    __stcs(reinterpret_cast<uint4 *>(p), make_uint4(pack_bf16(f[0].x, f[0].y), pack_bf16(f[1].x, f[1].y),
+                                                    pack_bf16(f[2].x, f[2].y), pack_bf16(f[3].x, f[3].y)));
   }
 };
 template <>
 struct BnVec8<float> {
-  float4 a, b;
-  __device__ __forceinline__ void load(const float *p) {
-    a = __ldcs(reinterpret_cast<const float4 *>(p));
-    b = __ldcs(reinterpret_cast<const float4 *>(p) + 1);
+  __device__ __forceinline__ static void load(const float *p, float2 *f) {
+    const float4 a = reinterpret_cast<const float4 *>(p)[0], b = reinterpret_cast<const float4 *>(p)[1];
+    f[0] = tc::f2(a.x, a.y);
+    f[1] = tc::f2(a.z, a.w);
+    f[2] = tc::f2(b.x, b.y);
+    f[3] = tc::f2(b.z, b.w);
   }
-  __device__ __forceinline__ void get(float *f) const {
-    f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
-    f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
-  }
-  __device__ __forceinline__ static void store(float *p, const float *f) {
-    __stcs(reinterpret_cast<float4 *>(p), make_float4(f[0], f[1], f[2], f[3]));
-    __stcs(reinterpret_cast<float4 *>(p) + 1, make_float4(f[4], f[5], f[6], f[7]));
+  __device__ __forceinline__ static void store(float *p, const float2 *f) {
+    __stcs(reinterpret_cast<float4 *>(p), make_float4(f[0].x, f[0].y, f[1].x, f[1].y));
+    __stcs(reinterpret_cast<float4 *>(p) + 1, make_float4(f[2].x, f[2].y, f[3].x, f[3].y));
   }
 };
+__device__ __forceinline__ float2 both(float x) { return tc::f2(x, x); }
+__device__ __forceinline__ float2 add2(float2 a, float2 b) { return tc::fma2(a, both(1.f), b); }
 
 __device__ __forceinline__ float param_at(const void *p, int64_t i, int f32) {
   return f32 ? static_cast<const float *>(p)[i] : __bfloat162float(static_cast<const __nv_bfloat16 *>(p)[i]);
 }
 // Eight parameters from element i on (i a multiple of 8).
-__device__ __forceinline__ void param8(const void *p, int64_t i, int f32, float *f) {
-  if (f32) {
-    const float4 a = __ldg(reinterpret_cast<const float4 *>(static_cast<const float *>(p) + i));
-    const float4 b = __ldg(reinterpret_cast<const float4 *>(static_cast<const float *>(p) + i) + 1);
-    f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w; f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
-  } else {
-    BnVec8<__nv_bfloat16> v;
-    v.a = __ldg(reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(p) + i));
-    v.get(f);
-  }
+__device__ __forceinline__ void param8(const void *p, int64_t i, int f32, float2 *f) {
+  if (f32) BnVec8<float>::load(static_cast<const float *>(p) + i, f);
+  else BnVec8<__nv_bfloat16>::load(static_cast<const __nv_bfloat16 *>(p) + i, f);
 }
 
-// Sums K values over the threads of one row (`wpr` warps), the same on every
-// thread: a butterfly in each warp, then the warps' sums in warp order.  Rows
-// of a CTA use barriers of their own (1 + row slot); `buf` alternates between
-// two halves of `red`, so one barrier per reduction is enough.
-template <int K>
-__device__ __forceinline__ void row_sums(float (&v)[K], float *red, int &buf, int wpr, int warp_in_row, int sub) {
+// Folded parameters of 8 columns from c on: w (1 + scale), shift, gate w_post.
+__device__ __forceinline__ void fold_params(const BlockNormArgs &a, int b, int c, float2 (&A)[4], float2 (&B)[4], float2 (&G)[4]) {
+  float2 s[4];
 #pragma unroll
-  for (int i = 0; i < K; ++i) v[i] = warp_sum(v[i]);
-  if (wpr == 1) return;
-  float *half = red + buf * (kBnMaxThreads / 32) * 4 + sub * wpr * 4;
-  buf ^= 1;
-  if ((threadIdx.x & 31) == 0) {
+  for (int e = 0; e < 4; ++e) A[e] = both(1.f), B[e] = both(0.f), G[e] = both(1.f);
+  if (a.weight) param8(a.weight, c, a.param_f32, A);
+  if (a.scale) {
+    param8(a.scale, b * a.sscale + c, a.param_f32, s);
 #pragma unroll
-    for (int i = 0; i < K; ++i) half[warp_in_row * 4 + i] = v[i];
+    for (int e = 0; e < 4; ++e) A[e] = tc::mul2(A[e], add2(s[e], both(1.f)));
   }
-  asm volatile("bar.sync %0, %1;" ::"r"(1 + sub), "r"(wpr * 32) : "memory");
+  if (a.shift) param8(a.shift, b * a.sshift + c, a.param_f32, B);
+  if (a.post_weight) param8(a.post_weight, c, a.param_f32, G);
+  if (a.gate) {
+    param8(a.gate, b * a.sgate + c, a.param_f32, s);
 #pragma unroll
-  for (int i = 0; i < K; ++i) v[i] = 0.f;
-  for (int w = 0; w < wpr; ++w) {
-    const float4 t = *reinterpret_cast<const float4 *>(half + 4 * w);
-    const float tv[4] = {t.x, t.y, t.z, t.w};
-#pragma unroll
-    for (int i = 0; i < K; ++i) v[i] += tv[i];
+    for (int e = 0; e < 4; ++e) G[e] = tc::mul2(G[e], s[e]);
   }
 }
+__device__ __forceinline__ float sum8(const float2 (&x)[4]) {
+  const float2 s = add2(add2(x[0], x[1]), add2(x[2], x[3]));
+  return s.x + s.y;
+}
+__device__ __forceinline__ void shift8(float2 (&x)[4], float m) {
+#pragma unroll
+  for (int e = 0; e < 4; ++e) x[e] = add2(x[e], both(-m));
+}
+__device__ __forceinline__ float2 dot8(const float2 (&x)[4], const float2 (&y)[4], float2 q) {
+#pragma unroll
+  for (int e = 0; e < 4; ++e) q = tc::fma2(x[e], y[e], q);
+  return q;
+}
 
-// Column parameters of sequence b for this thread's columns.
+// The run of rows [r0, r1) of sequence b that slot blockIdx.x stands for.
+__device__ __forceinline__ bool bn_rows(const BlockNormArgs &a, int &b, int &r0, int &r1) {
+  int64_t piece;
+  check_sequence(a.seq, blockIdx.x);
+  b = find_sequence(a.seq, blockIdx.x, 1, a.unit, piece);
+  int begin, len;
+  if (!sequence_rows(a.seq, b, begin, len)) return false;
+  if (piece < 0 || piece * a.unit >= len) return false;
+  r0 = begin + (int)piece * a.unit;
+  r1 = min(begin + len, r0 + a.unit);
+  return true;
+}
+
+// ---- forward -------------------------------------------------------------------
+// Row group `sub` of the CTA: wpr warps, a ring of single rows and, for wpr > 1,
+// named barrier 1 + sub and a table for sums.  V: vectors of 8 columns a thread
+// holds at most (a.vecs of them are used); vector v of a warp's lane covers
+// columns (warp vecs + v) 256 + 8 lane ...
 template <int V>
-struct BnColumns {
-  float A[8 * V], B[8 * V], G[8 * V];
-  __device__ __forceinline__ void load(const BlockNormArgs &a, int b, int t, int tpr) {
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const int c = (v * tpr + t) * 8;
-      float w[8], s[8];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) A[8 * v + e] = 1.f, B[8 * v + e] = 0.f, G[8 * v + e] = 1.f;
-      if (c >= a.C) continue;
-      if (a.weight) {
-        param8(a.weight, c, a.param_f32, w);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) A[8 * v + e] = w[e];
-      }
-      if (a.scale) {
-        param8(a.scale, b * a.sscale + c, a.param_f32, s);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) A[8 * v + e] *= 1.f + s[e];
-      }
-      if (a.shift) param8(a.shift, b * a.sshift + c, a.param_f32, B + 8 * v);
-      if (a.post_weight) param8(a.post_weight, c, a.param_f32, G + 8 * v);
-      if (a.gate) {
-        param8(a.gate, b * a.sgate + c, a.param_f32, s);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) G[8 * v + e] *= s[e];
-      }
-    }
+struct BnRow {
+  int wpr, sub, warp, n, buf;
+  float *red;          // [2][wpr][2]
+  __device__ __forceinline__ void sync() const {
+    if (wpr == 1) __syncwarp();
+    else asm volatile("bar.sync %0, %1;" ::"r"(1 + sub), "r"(wpr * 32) : "memory");
+  }
+  __device__ __forceinline__ float sum(float x) {
+    x = warp_sum(x);
+    if (wpr == 1) return x;
+    float *h = red + buf * wpr;
+    buf ^= 1;          // two halves used in turn: one barrier per sum
+    if ((threadIdx.x & 31) == 0) h[warp] = x;
+    sync();
+    float s = h[0];
+    for (int w = 1; w < wpr; ++w) s += h[w];
+    return s;
   }
 };
 
 template <typename TX, typename TY, int V>
-__global__ void __launch_bounds__(kBnMaxThreads) block_norm_fwd_kernel(const BlockNormArgs a, int wpr) {
-  __shared__ __align__(16) float red[2 * (kBnMaxThreads / 32) * 4];
-  const int warp = threadIdx.x >> 5;
-  const int sub = warp / wpr, wir = warp - sub * wpr;    // row slot of the CTA, warp within the row
-  const int rpc = (blockDim.x >> 5) / wpr;
-  const int tpr = wpr * 32, t = threadIdx.x - sub * tpr;
-  int64_t piece;
-  check_sequence(a.seq, blockIdx.x);
-  const int b = find_sequence(a.seq, blockIdx.x, 1, a.unit, piece);
-  int begin, len;
-  if (!sequence_rows(a.seq, b, begin, len)) return;
-  if (piece < 0 || piece * a.unit >= len) return;
-  const int r0 = begin + (int)piece * a.unit, r1 = min(begin + len, r0 + a.unit);
-
-  BnColumns<V> col;
-  col.load(a, b, t, tpr);
+__global__ void __launch_bounds__(kBnWarps * 32) block_norm_fwd_kernel(const BlockNormArgs a) {
+  extern __shared__ __align__(16) uint8_t bn_smem[];     // [A | B | G][C] fp32, rings
+  __shared__ uint64_t mbars[kBnWarps * kBnMaxStages];
+  __shared__ float red[2 * kBnWarps];
+  __shared__ int abort_flag;
+  int b, r0, r1;
+  if (!bn_rows(a, b, r0, r1)) return;
+  const int lane = threadIdx.x & 31;
   const TX *x = static_cast<const TX *>(a.x);
   const TY *y = static_cast<const TY *>(a.y);
-  TX *xo = static_cast<TX *>(a.x_out);
-  TY *h = static_cast<TY *>(a.h);
-  const float inv_c = 1.f / (float)a.C;
-  int buf = 0;
-
-  BnVec8<TX> xv[V];
-  BnVec8<TY> yv[V];
-  auto fetch = [&](int r) {
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const int c = (v * tpr + t) * 8;
-      if (c < a.C) {
-        xv[v].load(x + (int64_t)r * a.sx + c);
-        if (y) yv[v].load(y + (int64_t)r * a.sy + c);
-      }
-    }
+  BnRow<V> g;
+  g.wpr = a.wpr;
+  g.sub = (threadIdx.x >> 5) / a.wpr;
+  g.warp = (threadIdx.x >> 5) - g.sub * a.wpr;
+  g.red = red + 2 * g.sub * a.wpr;
+  g.buf = 0;
+  const int c0 = g.warp * a.vecs * 256 + lane * 8;
+  g.n = min(a.vecs, max(0, (a.C - c0 + 255) / 256));
+  const int bx = a.C * (int)sizeof(TX), stage_bytes = bx + (y ? a.C * (int)sizeof(TY) : 0);
+  uint8_t *ring = bn_smem + 12 * a.C + (size_t)g.sub * a.stages * stage_bytes;
+  const uint32_t ring_addr = smem_u32(ring), bars = smem_u32(mbars + g.sub * a.stages);
+  volatile int *abort = &abort_flag;
+  const bool lead = g.warp == 0 && lane == 0 && g.sub < a.groups;
+  if (lead) {
+    for (int i = 0; i < a.stages; ++i) tc::mbar_init(bars + 8u * i, 1);
+    tc::fence_barrier_init();
+  }
+  if (threadIdx.x == 0) *abort = 0;
+  __syncthreads();
+  const int first = r0 + g.sub, rows = g.sub < a.groups && first < r1 ? (r1 - first + a.groups - 1) / a.groups : 0;
+  int st_put = 0, st = 0;
+  uint32_t ph = 0;
+  auto fetch = [&](int it) {
+    const int64_t r = first + (int64_t)it * a.groups;
+    const uint32_t dst = ring_addr + st_put * stage_bytes, bar = bars + 8u * st_put;
+    tc::mbar_expect_tx(bar, stage_bytes);
+    tc::bulk_load(dst, x + r * a.sx, bx, bar);
+    if (y) tc::bulk_load(dst + bx, y + r * a.sy, stage_bytes - bx, bar);
+    if (++st_put == a.stages) st_put = 0;
   };
-  int r = r0 + sub;
-  if (r < r1) fetch(r);
-  for (; r < r1; r += rpc) {   // the rows of one slot run on their own barrier
-    float res[8 * V];
+  if (lead)
+    for (int it = 0; it < min(rows, a.stages); ++it) fetch(it);
+  float *const pA = reinterpret_cast<float *>(bn_smem), *const pB = pA + a.C, *const pG = pB + a.C;
+  for (int c = threadIdx.x * 8; c < a.C; c += blockDim.x * 8) {
+    float2 A[4], B[4], G[4];
+    fold_params(a, b, c, A, B, G);
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-      if ((v * tpr + t) * 8 < a.C) {
-        xv[v].get(res + 8 * v);
-      } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) res[8 * v + e] = 0.f;
-      }
+    for (int e = 0; e < 4; ++e) {
+      *reinterpret_cast<float2 *>(pA + c + 2 * e) = A[e];
+      *reinterpret_cast<float2 *>(pB + c + 2 * e) = B[e];
+      *reinterpret_cast<float2 *>(pG + c + 2 * e) = G[e];
     }
+  }
+  __syncthreads();
+  const float inv_c = 1.f / (float)a.C;
+  TX *xo = static_cast<TX *>(a.x_out) + first * a.sxo + c0;
+  TY *h = a.h ? static_cast<TY *>(a.h) + first * a.sh + c0 : nullptr;
+
+  for (int it = 0; it < rows; ++it) {
+    // A wait that runs out latches PRISM_ETIMEOUT; the warps go on (with whatever
+    // the ring holds), so that every barrier still sees all of its threads.
+    tc::mbar_wait(bars + 8u * st, ph, abort, a.wait_limit);
+    const TX *sx = reinterpret_cast<const TX *>(ring + st * stage_bytes) + c0;
+    const TY *sy = reinterpret_cast<const TY *>(ring + st * stage_bytes + bx) + c0;
+    if (++st == a.stages) st = 0, ph ^= 1;
+    float2 res[V][4];
     if (y) {
-      float f[8 * V];
-#pragma unroll
-      for (int v = 0; v < V; ++v) {
-        if ((v * tpr + t) * 8 < a.C) {
-          yv[v].get(f + 8 * v);
-        } else {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) f[8 * v + e] = 0.f;
-        }
-      }
-      if (r + rpc < r1) fetch(r + rpc);
       float mu = 0.f, rs = 1.f;
-      float s2[2] = {0.f, 0.f};
-      if (a.post != PRISM_NORM_NONE || a.y_norms) {
-#pragma unroll
-        for (int e = 0; e < 8 * V; ++e) s2[0] += f[e], s2[1] = fmaf(f[e], f[e], s2[1]);
-        row_sums(s2, red, buf, wpr, wir, sub);
-        if (a.y_norms && t == 0) a.y_norms[r] = sqrtf(s2[1]);
-      }
-      if (a.post == PRISM_NORM_RMS) {
-        rs = rsqrtf(s2[1] * inv_c + a.eps);
-      } else if (a.post == PRISM_NORM_LAYER) {
-        mu = s2[0] * inv_c;
-        float q[1] = {0.f};
+      if (a.y_norms) {
+        float2 q = both(0.f);
 #pragma unroll
         for (int v = 0; v < V; ++v)
-          if ((v * tpr + t) * 8 < a.C) {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) q[0] = fmaf(f[8 * v + e] - mu, f[8 * v + e] - mu, q[0]);
+          if (v < g.n) {
+            float2 f[4];
+            BnVec8<TY>::load(sy + v * 256, f);
+            q = dot8(f, f, q);
           }
-        row_sums(q, red, buf, wpr, wir, sub);
-        rs = rsqrtf(q[0] * inv_c + a.eps);
+        const float z = g.sum(q.x + q.y);
+        if (lead) a.y_norms[first + (int64_t)it * a.groups] = sqrtf(z);
       }
+      if (a.post != PRISM_NORM_NONE) {
+        if (a.post == PRISM_NORM_LAYER) {
+          float t = 0.f;
 #pragma unroll
-      for (int v = 0; v < V; ++v) {
-        const int c = (v * tpr + t) * 8;
-        if (c < a.C) {
-#pragma unroll
-          for (int e = 0; e < 8; ++e)
-            res[8 * v + e] = fmaf(col.G[8 * v + e], (f[8 * v + e] - mu) * rs, a.alpha * res[8 * v + e]);
-          if (xo) BnVec8<TX>::store(xo + (int64_t)r * a.sxo + c, res + 8 * v);
+          for (int v = 0; v < V; ++v)
+            if (v < g.n) {
+              float2 f[4];
+              BnVec8<TY>::load(sy + v * 256, f);
+              t += sum8(f);
+            }
+          mu = g.sum(t) * inv_c;
         }
+        float2 q = both(0.f);
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+          if (v < g.n) {
+            float2 f[4];
+            BnVec8<TY>::load(sy + v * 256, f);
+            shift8(f, mu);
+            q = dot8(f, f, q);
+          }
+        rs = rsqrtf(g.sum(q.x + q.y) * inv_c + a.eps);
       }
-    } else if (r + rpc < r1) {
-      fetch(r + rpc);
+#pragma unroll
+      for (int v = 0; v < V; ++v)
+        if (v < g.n) {
+          float2 f[4], G[4];
+          BnVec8<TX>::load(sx + v * 256, res[v]);
+          BnVec8<TY>::load(sy + v * 256, f);
+          BnVec8<float>::load(pG + c0 + v * 256, G);
+          shift8(f, mu);
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            res[v][e] = tc::fma2(tc::mul2(f[e], both(rs)), G[e], tc::mul2(res[v][e], both(a.alpha)));
+          BnVec8<TX>::store(xo + v * 256, res[v]);
+        }
+      xo += a.groups * a.sxo;
+    } else {
+#pragma unroll
+      for (int v = 0; v < V; ++v)
+        if (v < g.n) BnVec8<TX>::load(sx + v * 256, res[v]);
     }
-    if (!h) continue;
-    float mu = 0.f;
-    if (a.pre == PRISM_NORM_LAYER) {
-      float s[1] = {0.f};
+    // the row is in registers: the next one may land in its stage
+    g.sync();
+    if (lead && it + a.stages < rows) fetch(it + a.stages);
+    if (h) {
+      float mu = 0.f;
+      if (a.pre == PRISM_NORM_LAYER) {
+        float t = 0.f;
 #pragma unroll
-      for (int e = 0; e < 8 * V; ++e) s[0] += res[e];
-      row_sums(s, red, buf, wpr, wir, sub);
-      mu = s[0] * inv_c;
-    }
-    float q[1] = {0.f};
-#pragma unroll
-    for (int v = 0; v < V; ++v)
-      if ((v * tpr + t) * 8 < a.C) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) q[0] = fmaf(res[8 * v + e] - mu, res[8 * v + e] - mu, q[0]);
+        for (int v = 0; v < V; ++v)
+          if (v < g.n) t += sum8(res[v]);
+        mu = g.sum(t) * inv_c;
       }
-    row_sums(q, red, buf, wpr, wir, sub);
-    const float rs = rsqrtf(q[0] * inv_c + a.eps);
+      float2 q = both(0.f);
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const int c = (v * tpr + t) * 8;
-      if (c < a.C) {
-        float o[8];
+      for (int v = 0; v < V; ++v)
+        if (v < g.n) {
+          shift8(res[v], mu);
+          q = dot8(res[v], res[v], q);
+        }
+      const float rs = rsqrtf(g.sum(q.x + q.y) * inv_c + a.eps);
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-          o[e] = fmaf((res[8 * v + e] - mu) * rs, col.A[8 * v + e], col.B[8 * v + e]);
-        BnVec8<TY>::store(h + (int64_t)r * a.sh + c, o);
-      }
+      for (int v = 0; v < V; ++v)
+        if (v < g.n) {
+          float2 A[4], o[4];
+          BnVec8<float>::load(pA + c0 + v * 256, A);
+          BnVec8<float>::load(pB + c0 + v * 256, o);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[e] = tc::fma2(tc::mul2(res[v][e], both(rs)), A[e], o[e]);
+          BnVec8<TY>::store(h + v * 256, o);
+        }
+      h += a.groups * a.sh;
     }
+  }
+  if (lead && *abort) {      // after a wait ran out: the copies still in flight land before the CTA exits
+    volatile int no_abort = 0;
+    for (int it = max(0, rows - a.stages); it < rows; ++it)
+      tc::mbar_wait(bars + 8u * (it % a.stages), (uint32_t)(it / a.stages) & 1u, &no_abort, a.wait_limit);
   }
 }
 
-// Backward.  With r = x_out, u = r - mean, xhat = u rs and d = dh w (1 + scale):
+// ---- backward --------------------------------------------------------------------
+// With r = x_out, u = r - mean, xhat = u rs and d = dh w (1 + scale):
 //   dr = rs (d - mean(d) - xhat mean(d xhat)) + dx_out   (mean(d): only with a mean)
 //   dx = alpha dr,  e = dr gate w_post,  dy = rs_y (e - mean(e) - yhat mean(e yhat))
 // and the column sums sum(dh xhat), sum(dh), sum(dr yhat), from which the
 // parameters' gradients follow (block_norm_params_kernel).  The statistics
 // are formed again from x_out and y, which the pass reads anyway: keeping
 // them would cost the forward a write and this pass a read.
-template <typename TX, typename TY, int V>
-__global__ void __launch_bounds__(kBnMaxThreads) block_norm_bwd_kernel(const BlockNormArgs a, int wpr) {
-  __shared__ __align__(16) float red[2 * (kBnMaxThreads / 32) * 4];
-  const int warp = threadIdx.x >> 5;
-  const int sub = warp / wpr, wir = warp - sub * wpr;
-  const int rpc = (blockDim.x >> 5) / wpr;
-  const int tpr = wpr * 32, t = threadIdx.x - sub * tpr;
-  int64_t piece;
-  check_sequence(a.seq, blockIdx.x);
-  const int b = find_sequence(a.seq, blockIdx.x, 1, a.unit, piece);
-  int begin, len;
-  if (!sequence_rows(a.seq, b, begin, len)) return;
-  if (piece < 0 || piece * a.unit >= len) return;
-  const int r0 = begin + (int)piece * a.unit, r1 = min(begin + len, r0 + a.unit);
+//
+// R rows at a time (2; 1 beyond 4096 channels): a thread owns the same 8 (or 16)
+// columns of every row and sums the R rows' statistics together, so one butterfly
+// and one barrier serve several values.  Registers: at 16 columns a thread
+// (V = 2) the accumulators of the column sums and a row of values fill them, so
+// there the folded parameters live in shared memory.
+//
+// Sums over a warp of K values (a power of two) with few shuffles: lanes that
+// pair up keep half of the values each, so 4 values take 6 shuffles, not 20.
+// Lane 32 i / K returns the sum of value i.
+template <int K>
+__device__ __forceinline__ float warp_sums(float (&v)[K]) {
+  int n = K;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    if (n > 1) {
+      n >>= 1;
+      const bool hi = threadIdx.x & o;
+#pragma unroll
+      for (int i = 0; i < n; ++i) {
+        const float keep = hi ? v[i + n] : v[i], send = hi ? v[i] : v[i + n];
+        v[i] = keep + __shfl_xor_sync(0xffffffffu, send, o);
+      }
+    } else {
+      v[0] += __shfl_xor_sync(0xffffffffu, v[0], o);
+    }
+  }
+  return v[0];
+}
 
-  BnColumns<V> col;
-  col.load(a, b, t, tpr);
+// Row group `sub` of the CTA: its threads, its ring (stages of R rows) and its
+// barrier, and the sums over a row.
+template <int V, int R>
+struct BnGroup {
+  int wpr, sub, warp, t, tpr;          // warps per row, group, warp of the group, thread of the group, threads
+  int n;                               // vectors of a row that this thread owns
+  int row_bytes[4], off[4], bytes_per_row, stage_bytes, stages;
+  uint8_t *ring;
+  uint32_t ring_addr, bars;
+  float *red;                          // [2][wpr][8]
+  int buf, st_get, st_put, ph;         // stage to read and its phase, stage to fill
+  volatile int *abort;
+  uint32_t limit;
+
+  // bytes[k]: of a row of the k-th tensor of the ring, 0 for none.
+  __device__ __forceinline__ void init(const BlockNormArgs &a, const int (&bytes)[4], uint8_t *smem, uint64_t *mbars,
+                                       float *reds, volatile int *ab) {
+    wpr = a.wpr;
+    sub = (threadIdx.x >> 5) / wpr;
+    warp = (threadIdx.x >> 5) - sub * wpr;
+    tpr = wpr * 32;
+    t = threadIdx.x - sub * tpr;
+    n = 0;
+#pragma unroll
+    for (int v = 0; v < V; ++v) n += column(v) < a.C ? 1 : 0;
+    bytes_per_row = 0;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      row_bytes[k] = bytes[k];
+      off[k] = bytes_per_row * R;
+      bytes_per_row += bytes[k];
+    }
+    stage_bytes = bytes_per_row * R;
+    stages = a.stages;
+    ring = smem + (size_t)sub * stages * stage_bytes;
+    ring_addr = smem_u32(ring);
+    bars = smem_u32(mbars + sub * stages);
+    red = reds + sub * 2 * wpr * 8;
+    buf = st_get = st_put = ph = 0;
+    abort = ab;
+    limit = a.wait_limit;
+    if (t == 0) {
+      for (int i = 0; i < stages; ++i) tc::mbar_init(bars + 8u * i, 1);
+      tc::fence_barrier_init();
+    }
+    if (threadIdx.x == 0) *abort = 0;
+    __syncthreads();
+  }
+  __device__ __forceinline__ int column(int v) const { return (warp * V + v) * 256 + (threadIdx.x & 31) * 8; }
+  // All threads of the group: what they did before is visible after.
+  __device__ __forceinline__ void sync() const {
+    if (wpr == 1) __syncwarp();
+    else asm volatile("bar.sync %0, %1;" ::"r"(1 + sub), "r"(tpr) : "memory");
+  }
+  // Thread 0 of the group: copies the next `rows` rows into the next stage; src and
+  // step: row 0 of each tensor and the bytes from a row to the next.
+  __device__ __forceinline__ void fetch(int rows, const uint8_t *const (&src)[4], const int64_t (&step)[4]) {
+    const uint32_t bar = bars + 8u * st_put;
+    tc::mbar_expect_tx(bar, rows * bytes_per_row);
+    const uint32_t dst = ring_addr + st_put * stage_bytes;
+    for (int i = 0; i < rows; ++i) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (row_bytes[k]) tc::bulk_load(dst + off[k] + i * row_bytes[k], src[k] + i * step[k], row_bytes[k], bar);
+    }
+    if (++st_put == stages) st_put = 0;
+  }
+  // The next stage.  A wait that runs out latches PRISM_ETIMEOUT; the group goes on
+  // (with whatever the ring holds), so that every barrier still sees all threads.
+  __device__ __forceinline__ const uint8_t *next() {
+    const int st = st_get;
+    tc::mbar_wait(bars + 8u * st, (uint32_t)ph, abort, limit);
+    if (++st_get == stages) st_get = 0, ph ^= 1;
+    return ring + st * stage_bytes;
+  }
+  // After a wait ran out: the copies still in flight land before the CTA exits.
+  __device__ __forceinline__ void drain(int batches) const {
+    if (t != 0 || !*abort) return;
+    volatile int no_abort = 0;
+    for (int it = max(0, batches - stages); it < batches; ++it)
+      tc::mbar_wait(bars + 8u * (it % stages), (uint32_t)(it / stages) & 1u, &no_abort, limit);
+  }
+  // This thread's elements of row i of tensor k of a stage, zeros past the end.
+  template <typename T>
+  __device__ __forceinline__ void read(const uint8_t *stage, int k, int i, float2 (&f)[V][4]) const {
+    const T *p = reinterpret_cast<const T *>(stage + off[k] + i * row_bytes[k]) + column(0);
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      if (v < n) {
+        BnVec8<T>::load(p + v * 256, f[v]);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) f[v][e] = both(0.f);
+      }
+    }
+  }
+  __device__ __forceinline__ float total(const float2 (&x)[V][4]) const {
+    float s = 0.f;
+#pragma unroll
+    for (int v = 0; v < V; ++v) s += sum8(x[v]);
+    return s;
+  }
+  __device__ __forceinline__ float squares(const float2 (&x)[V][4]) const {
+    float2 q = both(0.f);
+#pragma unroll
+    for (int v = 0; v < V; ++v) q = dot8(x[v], x[v], q);
+    return q.x + q.y;
+  }
+  // x - m where this thread owns columns (0 stays 0 past the end).
+  __device__ __forceinline__ void subtract(float2 (&x)[V][4], float m) const {
+#pragma unroll
+    for (int v = 0; v < V; ++v) shift8(x[v], v < n ? m : 0.f);
+  }
+  // Sums of K values over the group, the same on every thread, in a fixed order: a
+  // butterfly in each warp, then the warps in order.  The table has two halves
+  // used in turn, so one barrier per exchange is enough.
+  template <int K>
+  __device__ __forceinline__ void sums(float (&v)[K]) {
+    const int lane = threadIdx.x & 31;
+    const float x = warp_sums(v);
+    if (wpr == 1) {
+#pragma unroll
+      for (int i = 0; i < K; ++i) v[i] = __shfl_sync(0xffffffffu, x, i * (32 / K));
+      return;
+    }
+    float *h = red + buf * wpr * 8;
+    buf ^= 1;
+    if (lane % (32 / K) == 0) h[warp * 8 + lane / (32 / K)] = x;
+    sync();
+#pragma unroll
+    for (int i = 0; i < K; ++i) v[i] = 0.f;
+    for (int w = 0; w < wpr; ++w, h += 8) {
+#pragma unroll
+      for (int i = 0; i < K; i += 2) {
+        const float2 y = *reinterpret_cast<const float2 *>(h + i);
+        v[i] += y.x;
+        v[i + 1] += y.y;
+      }
+    }
+  }
+};
+
+// Rows per batch: registers hold R rows of values beside the column sums.
+constexpr int bn_bwd_rows(int V) { return V == 1 ? 2 : 1; }
+
+template <typename TX, typename TY, int V>
+__global__ void __launch_bounds__(kBnMaxThreads) block_norm_bwd_kernel(const BlockNormArgs a) {
+  constexpr int R = bn_bwd_rows(V);
+  extern __shared__ __align__(16) uint8_t bn_smem[];
+  __shared__ uint64_t mbars[kBnMaxGroups * kBnMaxStages];
+  __shared__ __align__(16) float red[2 * (kBnMaxThreads / 32) * 8];
+  __shared__ int ab;
+  int b, r0, r1;
+  if (!bn_rows(a, b, r0, r1)) return;
+
   const TX *xo = static_cast<const TX *>(a.x_out), *dxo = static_cast<const TX *>(a.dx_out);
   const TY *y = static_cast<const TY *>(a.y), *dh = static_cast<const TY *>(a.dh);
   TX *dx = static_cast<TX *>(a.dx);
   TY *dy = static_cast<TY *>(a.dy);
-  const float inv_c = 1.f / (float)a.C;
-  int buf = 0;
-  float p1[8 * V], p2[8 * V], p3[8 * V];
+  BnGroup<V, R> g;
+  const int rx = a.C * (int)sizeof(TX), ry = a.C * (int)sizeof(TY);
+  const int bytes[4] = {dh ? rx : 0, dh ? ry : 0, dxo ? rx : 0, y ? ry : 0};
+  float *const params = reinterpret_cast<float *>(bn_smem);      // V = 2: [A | G][C]
+  g.init(a, bytes, bn_smem + (V == 2 ? 8 * a.C : 0), mbars, red, &ab);
+  // the group's rows are consecutive
+  const int per = (r1 - r0 + a.groups - 1) / a.groups;
+  const int first = r0 + g.sub * per, rows = max(0, min(per, r1 - first)), batches = (rows + R - 1) / R;
+  const int64_t step[4] = {a.sxo * (int64_t)sizeof(TX), a.sdh * (int64_t)sizeof(TY), a.sdxo * (int64_t)sizeof(TX),
+                           a.sy * (int64_t)sizeof(TY)};
+  auto fetch = [&](int it) {
+    const int64_t r = first + (int64_t)it * R;
+    const uint8_t *const src[4] = {
+        reinterpret_cast<const uint8_t *>(xo + r * a.sxo), reinterpret_cast<const uint8_t *>(dh + r * a.sdh),
+        reinterpret_cast<const uint8_t *>(dxo + r * a.sdxo), reinterpret_cast<const uint8_t *>(y + r * a.sy)};
+    g.fetch(min(R, rows - it * R), src, step);
+  };
+  if (g.t == 0)
+    for (int it = 0; it < min(batches, a.stages); ++it) fetch(it);
+  float2 A1[4], G1[4];      // V = 1
 #pragma unroll
-  for (int e = 0; e < 8 * V; ++e) p1[e] = p2[e] = p3[e] = 0.f;
-
-  BnVec8<TX> xv[V], gv[V];
-  BnVec8<TY> yv[V], hv[V];
-  auto fetch = [&](int r) {
+  for (int e = 0; e < 4; ++e) A1[e] = G1[e] = both(0.f);
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const int c = (v * tpr + t) * 8;
-      if (c < a.C) {
-        if (dh) {
-          xv[v].load(xo + (int64_t)r * a.sxo + c);
-          hv[v].load(dh + (int64_t)r * a.sdh + c);
+  for (int v = 0; v < V; ++v)
+    if (v < g.n) {
+      float2 A[4], B[4], G[4];
+      fold_params(a, b, g.column(v), A, B, G);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        if constexpr (V == 1) {
+          A1[e] = A[e];
+          G1[e] = G[e];
+        } else {            // a thread reads only what it wrote
+          *reinterpret_cast<float2 *>(params + g.column(v) + 2 * e) = A[e];
+          *reinterpret_cast<float2 *>(params + a.C + g.column(v) + 2 * e) = G[e];
         }
-        if (dxo) gv[v].load(dxo + (int64_t)r * a.sdxo + c);
-        if (y) yv[v].load(y + (int64_t)r * a.sy + c);
       }
+    }
+  auto parameter = [&](int which, int v, float2 (&p)[4]) {
+    if constexpr (V == 1) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) p[e] = which ? G1[e] : A1[e];
+    } else {
+      BnVec8<float>::load(params + which * a.C + g.column(v), p);
     }
   };
-  int r = r0 + sub;
-  if (r < r1) fetch(r);
-  for (; r < r1; r += rpc) {
-    float dr[8 * V], f[8 * V];
+  const float inv_c = 1.f / (float)a.C;
+  const bool cx = dh && a.pre == PRISM_NORM_LAYER, cy = y && a.post == PRISM_NORM_LAYER;
+  const bool py = y && a.post != PRISM_NORM_NONE;
+  const float al = y ? a.alpha : 1.f;
+  float2 p1[V][4], p2[V][4], p3[V][4];
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const bool in = (v * tpr + t) * 8 < a.C;
-      if (in && dxo) {
-        gv[v].get(dr + 8 * v);
-      } else {
+  for (int v = 0; v < V; ++v)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) dr[8 * v + e] = 0.f;
+    for (int e = 0; e < 4; ++e) p1[v][e] = p2[v][e] = p3[v][e] = both(0.f);
+  dx += first * a.sdx + g.column(0);
+  if (y) dy += first * a.sdy + g.column(0);
+
+  for (int it = 0; it < batches; ++it) {
+    const uint8_t *stage = g.next();
+    const int m = min(R, rows - it * R);     // rows of this batch; what is computed of others is not used
+    float2 u[R][V][4], f[R][V][4];           // x_out - mean, then dr; y - mean, then yhat
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+      if (y) g.template read<TY>(stage, 3, i, f[i]);
+      if (dh) g.template read<TX>(stage, 0, i, u[i]);
+    }
+    if (cx || cy) {
+      float s[2 * R];
+#pragma unroll
+      for (int i = 0; i < R; ++i) {
+        s[2 * i] = cx ? g.total(u[i]) : 0.f;
+        s[2 * i + 1] = cy ? g.total(f[i]) : 0.f;
       }
-      if (in && y) {
-        yv[v].get(f + 8 * v);
-      } else {
+      g.sums(s);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) f[8 * v + e] = 0.f;
+      for (int i = 0; i < R; ++i) {
+        if (cx) g.subtract(u[i], s[2 * i] * inv_c);
+        if (cy) g.subtract(f[i], s[2 * i + 1] * inv_c);
       }
     }
-    float u[8 * V], g[8 * V];
-    if (dh) {
+    float rs[R], c1[R], c2[R], rsy[R];
+    if (dh || py) {
+      float s[4 * R];       // squares of x_out - mean, of y - mean; sum(d), sum(d u)
 #pragma unroll
-      for (int v = 0; v < V; ++v) {
-        if ((v * tpr + t) * 8 < a.C) {
-          xv[v].get(u + 8 * v);
-          hv[v].get(g + 8 * v);
-        } else {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) u[8 * v + e] = g[8 * v + e] = 0.f;
-        }
-      }
-    }
-    if (r + rpc < r1) fetch(r + rpc);
-    // means
-    float mu = 0.f, muy = 0.f;
-    const bool lx = dh && a.pre == PRISM_NORM_LAYER, ly = y && a.post == PRISM_NORM_LAYER;
-    if (lx || ly) {
-      float s[2] = {0.f, 0.f};
-      if (lx) {
-#pragma unroll
-        for (int e = 0; e < 8 * V; ++e) s[0] += u[e];
-      }
-      if (ly) {
-#pragma unroll
-        for (int e = 0; e < 8 * V; ++e) s[1] += f[e];
-      }
-      row_sums(s, red, buf, wpr, wir, sub);
-      mu = s[0] * inv_c;
-      muy = s[1] * inv_c;
-    }
-    // centred squares, and the sums of the pre-norm's gradient
-    float s4[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-    for (int v = 0; v < V; ++v)
-      if ((v * tpr + t) * 8 < a.C) {
+      for (int i = 0; i < R; ++i) {
+        s[4 * i] = s[4 * i + 2] = s[4 * i + 3] = 0.f;
+        s[4 * i + 1] = py ? g.squares(f[i]) : 0.f;
         if (dh) {
+          s[4 * i] = g.squares(u[i]);
+          float2 d8[V][4], sd = both(0.f), sdu = both(0.f);
+          g.template read<TY>(stage, 1, i, d8);
 #pragma unroll
-          for (int e = 8 * v; e < 8 * v + 8; ++e) {
-            u[e] -= mu;
-            const float d = g[e] * col.A[e];
-            s4[0] = fmaf(u[e], u[e], s4[0]);
-            s4[1] += d;
-            s4[2] = fmaf(d, u[e], s4[2]);
-          }
-        }
-        if (y) {
+          for (int v = 0; v < V; ++v)
+            if (V == 1 || v < g.n) {
+              float2 A[4];
+              parameter(0, v, A);
 #pragma unroll
-          for (int e = 8 * v; e < 8 * v + 8; ++e) {
-            f[e] -= muy;
-            s4[3] = fmaf(f[e], f[e], s4[3]);
-          }
+              for (int e = 0; e < 4; ++e) {
+                d8[v][e] = tc::mul2(d8[v][e], A[e]);
+                sd = add2(d8[v][e], sd);
+              }
+              sdu = dot8(d8[v], u[i][v], sdu);
+            }
+          s[4 * i + 2] = sd.x + sd.y;
+          s[4 * i + 3] = sdu.x + sdu.y;
         }
       }
-    row_sums(s4, red, buf, wpr, wir, sub);
-    if (dh) {
-      const float rs = rsqrtf(s4[0] * inv_c + a.eps);
-      const float c1 = a.pre == PRISM_NORM_LAYER ? s4[1] * inv_c : 0.f;
-      const float c2 = s4[2] * rs * inv_c;    // mean(d xhat)
+      g.sums(s);
 #pragma unroll
-      for (int e = 0; e < 8 * V; ++e) {
-        const float xh = u[e] * rs, d = g[e] * col.A[e];
-        dr[e] += rs * (d - c1 - xh * c2);
-        p1[e] = fmaf(g[e], xh, p1[e]);
-        p2[e] += g[e];
+      for (int i = 0; i < R; ++i) {
+        rs[i] = rsqrtf(s[4 * i] * inv_c + a.eps);
+        rsy[i] = py ? rsqrtf(s[4 * i + 1] * inv_c + a.eps) : 1.f;
+        c1[i] = cx ? s[4 * i + 2] * inv_c : 0.f;
+        c2[i] = s[4 * i + 3] * rs[i] * inv_c;        // mean(d xhat)
+        if (py) {
+#pragma unroll
+          for (int v = 0; v < V; ++v)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) f[i][v][e] = tc::mul2(f[i][v][e], both(rsy[i]));
+        }
       }
+    } else {
+#pragma unroll
+      for (int i = 0; i < R; ++i) rs[i] = c1[i] = c2[i] = 0.f, rsy[i] = 1.f;
     }
-    float dxs[8 * V];
-    const float al = y ? a.alpha : 1.f;
 #pragma unroll
-    for (int e = 0; e < 8 * V; ++e) dxs[e] = al * dr[e];
+    for (int i = 0; i < R; ++i)
+      if (i < m) {
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const int c = (v * tpr + t) * 8;
-      if (c < a.C) BnVec8<TX>::store(dx + (int64_t)r * a.sdx + c, dxs + 8 * v);
-    }
-    if (!y) continue;
-    float m1 = 0.f, m2 = 0.f, rsy = 1.f;
-    if (a.post != PRISM_NORM_NONE) {
-      rsy = rsqrtf(s4[3] * inv_c + a.eps);
-      float s[2] = {0.f, 0.f};
+        for (int v = 0; v < V; ++v)
+          if (v < g.n) {
+            float2 o[4];
+            if (dxo) {
+              BnVec8<TX>::load(reinterpret_cast<const TX *>(stage + g.off[2] + i * g.row_bytes[2]) + g.column(v), o);
+            } else {
 #pragma unroll
-      for (int v = 0; v < V; ++v)
-        if ((v * tpr + t) * 8 < a.C) {
+              for (int e = 0; e < 4; ++e) o[e] = both(0.f);
+            }
+            if (dh) {
+              float2 A[4], d8[4];
+              parameter(0, v, A);
+              BnVec8<TY>::load(reinterpret_cast<const TY *>(stage + g.off[1] + i * g.row_bytes[1]) + g.column(v), d8);
 #pragma unroll
-          for (int e = 8 * v; e < 8 * v + 8; ++e) {
-            f[e] *= rsy;
-            const float de = dr[e] * col.G[e];
-            s[0] += de;
-            s[1] = fmaf(de, f[e], s[1]);
+              for (int e = 0; e < 4; ++e) {
+                const float2 xh = tc::mul2(u[i][v][e], both(rs[i]));
+                const float2 in = tc::fma2(xh, both(-c2[i]), tc::fma2(d8[e], A[e], both(-c1[i])));
+                o[e] = tc::fma2(both(rs[i]), in, o[e]);
+                p1[v][e] = tc::fma2(d8[e], xh, p1[v][e]);
+                p2[v][e] = add2(d8[e], p2[v][e]);
+              }
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              u[i][v][e] = o[e];
+              o[e] = tc::mul2(o[e], both(al));
+            }
+            BnVec8<TX>::store(dx + v * 256, o);
           }
-        }
-      row_sums(s, red, buf, wpr, wir, sub);
-      m1 = a.post == PRISM_NORM_LAYER ? s[0] * inv_c : 0.f;
-      m2 = s[1] * inv_c;
-    }
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const int c = (v * tpr + t) * 8;
-      if (c < a.C) {
-        float o[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const int k = 8 * v + e;
-          p3[k] = fmaf(dr[k], f[k], p3[k]);
-          o[e] = rsy * (dr[k] * col.G[k] - m1 - f[k] * m2);
-        }
-        BnVec8<TY>::store(dy + (int64_t)r * a.sdy + c, o);
+        dx += a.sdx;
       }
+    float s[2 * R];        // sum(e), sum(e yhat)
+#pragma unroll
+    for (int i = 0; i < 2 * R; ++i) s[i] = 0.f;
+    if (py) {
+#pragma unroll
+      for (int i = 0; i < R; ++i) {
+        float2 s0 = both(0.f), s1 = both(0.f);
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+          if (v < g.n) {
+            float2 G[4];
+            parameter(1, v, G);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float2 de = tc::mul2(u[i][v][e], G[e]);
+              s0 = add2(de, s0);
+              s1 = tc::fma2(de, f[i][v][e], s1);
+            }
+          }
+        s[2 * i] = s0.x + s0.y;
+        s[2 * i + 1] = s1.x + s1.y;
+      }
+      g.sums(s);
+    }
+    if (!py || g.wpr == 1) g.sync();
+    // every thread of the group has read the stage: its next rows may land there
+    if (g.t == 0 && it + a.stages < batches) fetch(it + a.stages);
+    if (y) {
+#pragma unroll
+      for (int i = 0; i < R; ++i)
+        if (i < m) {
+          const float m1 = cy ? s[2 * i] * inv_c : 0.f, m2 = s[2 * i + 1] * inv_c;
+#pragma unroll
+          for (int v = 0; v < V; ++v)
+            if (v < g.n) {
+              float2 o[4], G[4];
+              parameter(1, v, G);
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                p3[v][e] = tc::fma2(u[i][v][e], f[i][v][e], p3[v][e]);
+                const float2 de = tc::fma2(u[i][v][e], G[e], both(-m1));
+                o[e] = tc::mul2(tc::fma2(f[i][v][e], both(-m2), de), both(rsy[i]));
+              }
+              BnVec8<TY>::store(dy + v * 256, o);
+            }
+          dy += a.sdy;
+        }
     }
   }
-  if (a.part) {
-    float *out = a.part + ((int64_t)blockIdx.x * rpc + sub) * 3 * a.C;
+  g.drain(batches);
+  if (a.need) {
+    float *out = a.part + ((int64_t)blockIdx.x * a.groups + g.sub) * 3 * a.C;
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const int c = (v * tpr + t) * 8;
-      if (c < a.C) {
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          *reinterpret_cast<float4 *>(out + c + 4 * k) =
-              make_float4(p1[8 * v + 4 * k], p1[8 * v + 4 * k + 1], p1[8 * v + 4 * k + 2], p1[8 * v + 4 * k + 3]);
-          *reinterpret_cast<float4 *>(out + a.C + c + 4 * k) =
-              make_float4(p2[8 * v + 4 * k], p2[8 * v + 4 * k + 1], p2[8 * v + 4 * k + 2], p2[8 * v + 4 * k + 3]);
-          *reinterpret_cast<float4 *>(out + 2 * a.C + c + 4 * k) =
-              make_float4(p3[8 * v + 4 * k], p3[8 * v + 4 * k + 1], p3[8 * v + 4 * k + 2], p3[8 * v + 4 * k + 3]);
-        }
+    for (int v = 0; v < V; ++v)
+      if (v < g.n) {
+        float *o = out + g.column(v);
+        if (a.need & 1) BnVec8<float>::store(o, p1[v]);
+        if (a.need & 2) BnVec8<float>::store(o + a.C, p2[v]);
+        if (a.need & 4) BnVec8<float>::store(o + 2 * a.C, p3[v]);
       }
-    }
   }
 }
 
-// Parameter gradients from the column sums, in two steps with a fixed order
-// of additions.  Step 1, one CTA per (32 columns, sequence): the sums of the
-// sequence's slots; per-sequence gradients leave here.
+// Parameter gradients from the column sums, one CTA per 32 columns and
+//   blockIdx.y = 0       what is summed over all sequences: the weights, and gate,
+//                        scale and shift where the sequences share them
+//   blockIdx.y = 1 + b   gate, scale and shift of sequence b
+// The warps' sums are added in order: the additions have a fixed order.
 struct BnParamArgs {
   Offsets seq;
-  int C, unit, rpc, param_f32;
-  const float *part;         // [slots * rpc][3][C]
-  float *sums;               // [seqs][3][C]
+  int C, unit, groups, param_f32, need;
+  const float *part;         // [slots * groups][3][C]
   const void *weight, *post_weight, *gate, *scale;
   int64_t sgate, sscale;
   void *dweight, *dpost_weight;               // [C]
@@ -492,62 +772,54 @@ __device__ __forceinline__ void put_param(void *p, int64_t i, float v, int f32) 
   else static_cast<__nv_bfloat16 *>(p)[i] = __float2bfloat16_rn(v);
 }
 
-__global__ void __launch_bounds__(1024) block_norm_sums_kernel(const BnParamArgs a) {
-  __shared__ float sh[32][3][33];
+constexpr int kBnParamWarps = 16;
+__global__ void __launch_bounds__(kBnParamWarps * 32) block_norm_params_kernel(const BnParamArgs a) {
+  __shared__ float sh[kBnParamWarps][5][32];
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-  const int c = blockIdx.x * 32 + lane, b = blockIdx.y;
-  int begin, len;
-  const bool ok = sequence_rows(a.seq, b, begin, len);
-  const int64_t first = ((int64_t)begin / a.unit + b) * a.rpc;
-  const int64_t n = ok ? (int64_t)((len + a.unit - 1) / a.unit) * a.rpc : 0;
-  float s[3] = {0.f, 0.f, 0.f};
-  if (c < a.C) {
-    for (int64_t i = w; i < n; i += 32) {
-      const float *p = a.part + (first + i) * 3 * a.C + c;
-      s[0] += p[0];
-      s[1] += p[a.C];
-      s[2] += p[2 * (int64_t)a.C];
+  const int c = blockIdx.x * 32 + lane;
+  const bool in = c < a.C;
+  const bool all = blockIdx.y == 0;
+  const int b0 = all ? 0 : (int)blockIdx.y - 1, b1 = all ? a.seq.seqs : (int)blockIdx.y;
+  // few sequences have many runs of rows each, which the warps share out; many
+  // have few, and a warp takes a sequence
+  const int over = b1 - b0 > kBnParamWarps ? kBnParamWarps : 1, each = kBnParamWarps / over;
+  // plain sums of the three kinds, and the sums that the weights' gradients take
+  float s[5] = {0.f, 0.f, 0.f, 0.f, 0.f};
+  for (int b = b0 + w / each; b < b1; b += over) {
+    int begin, len;
+    if (!in || !sequence_rows(a.seq, b, begin, len)) continue;
+    const float ws = all && a.dweight && a.scale ? 1.f + param_at(a.scale, b * a.sscale + c, a.param_f32) : 1.f;
+    const float wg = all && a.dpost_weight && a.gate ? param_at(a.gate, b * a.sgate + c, a.param_f32) : 1.f;
+    const float *p = a.part + ((int64_t)begin / a.unit + b) * a.groups * 3 * a.C + c;
+    const int n = (len + a.unit - 1) / a.unit * a.groups;
+    const bool k0 = a.need & 1, k1 = a.need & 2, k2 = a.need & 4;
+    float t[3] = {0.f, 0.f, 0.f};
+#pragma unroll 4
+    for (int i = w % each; i < n; i += each) {
+      const float *q = p + (int64_t)i * 3 * a.C;
+      if (k0) t[0] += q[0];
+      if (k1) t[1] += q[a.C];
+      if (k2) t[2] += q[2 * (int64_t)a.C];
     }
+#pragma unroll
+    for (int k = 0; k < 3; ++k) s[k] += t[k];
+    s[3] = fmaf(ws, t[0], s[3]);
+    s[4] = fmaf(wg, t[2], s[4]);
   }
 #pragma unroll
-  for (int k = 0; k < 3; ++k) sh[w][k][lane] = s[k];
+  for (int k = 0; k < 5; ++k) sh[w][k][lane] = s[k];
   __syncthreads();
-  if (w < 3) {
-    float v = 0.f;
-    for (int i = 0; i < 32; ++i) v += sh[i][w][lane];
-    if (c < a.C) {
-      a.sums[((int64_t)b * 3 + w) * a.C + c] = v;
-      const int64_t at = (int64_t)b * a.C + c;
-      if (w == 0 && a.dscale && a.per_scale)
-        put_param(a.dscale, at, a.weight ? v * param_at(a.weight, c, a.param_f32) : v, a.param_f32);
-      if (w == 1 && a.dshift && a.per_shift) put_param(a.dshift, at, v, a.param_f32);
-      if (w == 2 && a.dgate && a.per_gate)
-        put_param(a.dgate, at, a.post_weight ? v * param_at(a.post_weight, c, a.param_f32) : v, a.param_f32);
-    }
-  }
-}
-
-// Step 2, one thread per column: what is summed over the sequences.
-__global__ void __launch_bounds__(128) block_norm_params_kernel(const BnParamArgs a) {
-  const int c = blockIdx.x * 128 + threadIdx.x;
-  if (c >= a.C) return;
-  float dw = 0.f, dpw = 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f;
-  for (int b = 0; b < a.seq.seqs; ++b) {
-    const float *p = a.sums + (int64_t)b * 3 * a.C + c;
-    const float q1 = p[0], q2 = p[a.C], q3 = p[2 * (int64_t)a.C];
-    s1 += q1;
-    s2 += q2;
-    s3 += q3;
-    dw = fmaf(a.scale ? 1.f + param_at(a.scale, b * a.sscale + c, a.param_f32) : 1.f, q1, dw);
-    dpw = fmaf(a.gate ? param_at(a.gate, b * a.sgate + c, a.param_f32) : 1.f, q3, dpw);
-  }
-  if (a.dweight) put_param(a.dweight, c, dw, a.param_f32);
-  if (a.dpost_weight) put_param(a.dpost_weight, c, dpw, a.param_f32);
-  if (a.dscale && !a.per_scale)
-    put_param(a.dscale, c, a.weight ? s1 * param_at(a.weight, c, a.param_f32) : s1, a.param_f32);
-  if (a.dshift && !a.per_shift) put_param(a.dshift, c, s2, a.param_f32);
-  if (a.dgate && !a.per_gate)
-    put_param(a.dgate, c, a.post_weight ? s3 * param_at(a.post_weight, c, a.param_f32) : s3, a.param_f32);
+  if (w >= 5 || !in) return;
+  float v = 0.f;
+  for (int i = 0; i < kBnParamWarps; ++i) v += sh[i][w][lane];
+  const int64_t at = all ? c : (int64_t)b0 * a.C + c;
+  if (w == 0 && a.dscale && (a.per_scale != 0) != all)
+    put_param(a.dscale, at, a.weight ? v * param_at(a.weight, c, a.param_f32) : v, a.param_f32);
+  if (w == 1 && a.dshift && (a.per_shift != 0) != all) put_param(a.dshift, at, v, a.param_f32);
+  if (w == 2 && a.dgate && (a.per_gate != 0) != all)
+    put_param(a.dgate, at, a.post_weight ? v * param_at(a.post_weight, c, a.param_f32) : v, a.param_f32);
+  if (w == 3 && all && a.dweight) put_param(a.dweight, c, v, a.param_f32);
+  if (w == 4 && all && a.dpost_weight) put_param(a.dpost_weight, c, v, a.param_f32);
 }
 
 }  // namespace prism

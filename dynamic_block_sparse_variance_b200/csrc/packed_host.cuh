@@ -183,7 +183,7 @@ static int check_norm(const prism_norm_params *p) {
   if (!p) return fail(PRISM_EINVAL, "norm params is NULL");
   if (p->rows < 0 || p->rows > 0x7fffff00LL) return fail(PRISM_EINVAL, "block_norm: rows must be in [0, 2^31 - 256]");
   if (p->seqs < 1) return fail(PRISM_EINVAL, "block_norm: seqs must be positive");
-  if (p->seqs > 65535) return fail(PRISM_EINVAL, "block_norm: at most 65535 sequences");
+  if (p->seqs > 65534) return fail(PRISM_EINVAL, "block_norm: at most 65534 sequences");
   if (p->channels < 8 || p->channels % 8 || p->channels > PRISM_NORM_MAX_CHANNELS)
     return fail(PRISM_EINVAL, "block_norm: channels must be a multiple of 8 in [8, 8192]");
   if (!is_float_type(p->stream_dtype) || !is_float_type(p->branch_dtype) || !is_float_type(p->param_dtype))
@@ -223,61 +223,99 @@ static int norm_args(const prism_norm_params *p, const int32_t *off, const void 
   a->sgate = p->gate_stride;
   a->sscale = p->scale_stride;
   a->sshift = p->shift_stride;
-  a->part = nullptr;
-  a->y_norms = nullptr;
-  a->h = a->x_out = a->dx = a->dy = nullptr;
-  a->x = a->y = a->dh = a->dx_out = nullptr;
+  a->wait_limit = wait_limit();
   return PRISM_OK;
 }
 
-// Threads: 8 columns each up to 4096 channels, 16 beyond; narrow rows share a
-// CTA of about 256 threads.
-struct NormShape {
-  int vec, wpr, rpc, threads;
-  explicit NormShape(int C) {
-    vec = C > 8 * kBnMaxThreads ? 2 : 1;
-    wpr = (C + 256 * vec - 1) / (256 * vec);
-    rpc = std::max(1, 8 / wpr);
-    threads = wpr * rpc * 32;
-  }
-};
-static int norm_unit(int64_t rows, int rpc, int slots, int most) {
-  const int64_t u = (rows + slots - 1) / slots;
-  return (int)std::max<int64_t>(rpc, std::min<int64_t>(most, (u + rpc - 1) / rpc * rpc));
+// Launch shapes: one CTA per SM, whose rings take what shared memory the folded
+// parameters leave, and about as many runs of rows as there are SMs.
+constexpr int kBnSmem = 216 * 1024;
+static int type_bytes(int t) { return t == PRISM_F32 ? 4 : 2; }
+static int norm_unit(const prism_norm_params *p, int least) {
+  const int64_t wave = std::max<int64_t>(1, 148 - p->seqs);      // a sequence's last run may be short
+  const int64_t u = (p->rows + wave - 1) / wave;
+  return (int)std::max<int64_t>(least, u);
 }
-
-struct NormBwdWs {
-  NormShape shape;
-  int unit;
+// Forward: a row in the registers of one warp up to 2048 channels (8 vectors of
+// 8 columns a thread), of 2 to 4 warps beyond.
+struct NormFwdShape {
+  int wpr, groups, vecs, V, stages, unit, threads;
+  size_t smem;
   int64_t slots;
-  size_t part, sums, total;
-  explicit NormBwdWs(const prism_norm_params *p) : shape(p->channels) {
-    unit = norm_unit(p->rows, shape.rpc, 148 * 2, 1 << 20);
+  NormFwdShape(const prism_norm_params *p, bool with_y) {
+    const int C = p->channels;
+    wpr = (C + 2047) / 2048;
+    vecs = (C + 256 * wpr - 1) / (256 * wpr);
+    V = vecs <= 1 ? 1 : vecs <= 2 ? 2 : vecs <= 4 ? 4 : 8;
+    const int row = C * (type_bytes(p->stream_dtype) + (with_y ? type_bytes(p->branch_dtype) : 0));
+    groups = std::max(1, std::min(kBnWarps / wpr, (kBnSmem - 12 * C) / row));
+    unit = norm_unit(p, 1);
+    groups = std::min(groups, unit);
+    stages = std::max(1, std::min({kBnMaxStages, (kBnSmem - 12 * C) / (groups * row), (unit + groups - 1) / groups}));
+    smem = (size_t)12 * C + (size_t)groups * stages * row;
+    // more warps than rows need still share the folding of the parameters
+    threads = std::max(groups * wpr, std::min(kBnWarps, C / 256)) * 32;
     slots = slot_bound(p->rows, p->seqs, 1, unit);
-    part = 0;
-    sums = align256((size_t)slots * shape.rpc * 3 * p->channels * 4);
-    total = sums + align256((size_t)p->seqs * 3 * p->channels * 4);
+  }
+};
+// Backward: 8 columns a thread up to 4096 channels, 16 beyond; narrow rows share
+// a CTA of about 256 threads.  The kernel's registers let an SM hold 16 warps,
+// which with the rings gives the CTAs per SM and, one wave of them, the rows
+// per CTA.  The stages have room for all four tensors, whichever a call gives.
+struct NormBwdShape {
+  int V, wpr, groups, threads, stages, unit;
+  size_t smem;
+  int64_t slots;
+  explicit NormBwdShape(const prism_norm_params *p) {
+    const int C = p->channels;
+    V = C > 8 * kBnMaxThreads ? 2 : 1;
+    wpr = (C + 256 * V - 1) / (256 * V);
+    groups = std::max(1, 8 / wpr);
+    threads = wpr * groups * 32;
+    const int batch = bn_bwd_rows(V);
+    const int stage = C * 2 * (type_bytes(p->stream_dtype) + type_bytes(p->branch_dtype)) * groups * batch;
+    const int fixed = V == 2 ? 8 * C : 0;
+    const int ctas = std::max(1, std::min(16 / (wpr * groups), 200 * 1024 / (2 * stage + fixed + 2048)));
+    stages = std::max(1, std::min(kBnMaxStages, (200 * 1024 / ctas - fixed - 2048) / stage));
+    smem = (size_t)stages * stage + fixed;
+    const int64_t wave = std::max<int64_t>(1, (int64_t)148 * ctas - p->seqs);
+    unit = (int)std::max<int64_t>(2 * groups, (p->rows + wave - 1) / wave);
+    const int whole = batch * groups;      // whole batches, unless the rows are few
+    if (unit >= whole) unit = (unit + whole - 1) / whole * whole;
+    slots = slot_bound(p->rows, p->seqs, 1, unit);
   }
 };
 
+template <typename TX, typename TY, int V>
+static int launch_norm_fwd_v(const NormFwdShape &s, const BlockNormArgs &a, cudaStream_t st) {
+  cudaFuncSetAttribute(block_norm_fwd_kernel<TX, TY, V>, cudaFuncAttributeMaxDynamicSharedMemorySize, kBnSmem);
+  PRISM_TRACED("block_norm_fwd_kernel", st, block_norm_fwd_kernel<TX, TY, V><<<(unsigned)s.slots, s.threads, s.smem, st>>>(a));
+  return PRISM_OK;
+}
 template <typename TX, typename TY>
 static int launch_norm_fwd(const prism_norm_params *p, BlockNormArgs &a, cudaStream_t st) {
-  const NormShape s(p->channels);
-  a.unit = norm_unit(p->rows, s.rpc, 148 * 8, 32 * s.rpc);
-  const unsigned grid = (unsigned)slot_bound(p->rows, p->seqs, 1, a.unit);
-  if (s.vec == 1)
-    PRISM_TRACED("block_norm_fwd_kernel", st, block_norm_fwd_kernel<TX, TY, 1><<<grid, s.threads, 0, st>>>(a, s.wpr));
-  else
-    PRISM_TRACED("block_norm_fwd_kernel", st, block_norm_fwd_kernel<TX, TY, 2><<<grid, s.threads, 0, st>>>(a, s.wpr));
+  const NormFwdShape s(p, a.y != nullptr);
+  a.unit = s.unit;
+  a.wpr = s.wpr;
+  a.groups = s.groups;
+  a.stages = s.stages;
+  a.vecs = s.vecs;
+  switch (s.V) {
+    case 1: return launch_norm_fwd_v<TX, TY, 1>(s, a, st);
+    case 2: return launch_norm_fwd_v<TX, TY, 2>(s, a, st);
+    case 4: return launch_norm_fwd_v<TX, TY, 4>(s, a, st);
+    default: return launch_norm_fwd_v<TX, TY, 8>(s, a, st);
+  }
+}
+template <typename TX, typename TY, int V>
+static int launch_norm_bwd_v(const NormBwdShape &s, const BlockNormArgs &a, cudaStream_t st) {
+  cudaFuncSetAttribute(block_norm_bwd_kernel<TX, TY, V>, cudaFuncAttributeMaxDynamicSharedMemorySize, kBnSmem);
+  PRISM_TRACED("block_norm_bwd_kernel", st, block_norm_bwd_kernel<TX, TY, V><<<(unsigned)s.slots, s.threads, s.smem, st>>>(a));
   return PRISM_OK;
 }
 template <typename TX, typename TY>
-static int launch_norm_bwd(const NormBwdWs &w, BlockNormArgs &a, cudaStream_t st) {
-  if (w.shape.vec == 1)
-    PRISM_TRACED("block_norm_bwd_kernel", st, block_norm_bwd_kernel<TX, TY, 1><<<(unsigned)w.slots, w.shape.threads, 0, st>>>(a, w.shape.wpr));
-  else
-    PRISM_TRACED("block_norm_bwd_kernel", st, block_norm_bwd_kernel<TX, TY, 2><<<(unsigned)w.slots, w.shape.threads, 0, st>>>(a, w.shape.wpr));
-  return PRISM_OK;
+static int launch_norm_bwd(const NormBwdShape &s, const BlockNormArgs &a, cudaStream_t st) {
+  return s.V == 1 ? launch_norm_bwd_v<TX, TY, 1>(s, a, st) : launch_norm_bwd_v<TX, TY, 2>(s, a, st);
 }
 
 }  // namespace prism
@@ -359,7 +397,7 @@ int prism_block_norm_fwd(const prism_norm_params *p, const void *x, const void *
                          const void *shift, void *x_out, void *h, float *y_norms, prism_stream stream) {
   int rc = check_norm(p);
   if (rc) return rc;
-  BlockNormArgs a;
+  BlockNormArgs a = {};
   rc = norm_args(p, off, post_weight, gate, weight, scale, shift, &a);
   if (rc) return rc;
   if (p->rows == 0) return PRISM_OK;
@@ -384,7 +422,8 @@ int prism_block_norm_workspace_size(const prism_norm_params *p, size_t *bytes) {
   int rc = check_norm(p);
   if (rc) return rc;
   if (!bytes) return fail(PRISM_EINVAL, "bytes is NULL");
-  *bytes = NormBwdWs(p).total;
+  const NormBwdShape s(p);
+  *bytes = align256((size_t)s.slots * s.groups * 3 * p->channels * 4);
   return PRISM_OK;
 }
 
@@ -395,7 +434,7 @@ int prism_block_norm_bwd(const prism_norm_params *p, const void *x_out, const vo
                          prism_stream stream) {
   int rc = check_norm(p);
   if (rc) return rc;
-  BlockNormArgs a;
+  BlockNormArgs a = {};
   rc = norm_args(p, off, post_weight, gate, weight, scale, nullptr, &a);
   if (rc) return rc;
   if (p->rows && ((!dh && !dx_out) || (dh && !x_out) || !dx || (y && !dy)))
@@ -403,19 +442,22 @@ int prism_block_norm_bwd(const prism_norm_params *p, const void *x_out, const vo
   if (!y && (dpost_weight || dgate)) return fail(PRISM_EINVAL, "block_norm: dpost_weight and dgate need y");
   for (const void *t : {x_out, y, dh, dx_out, (const void *)dx, (const void *)dy})
     if (!aligned16(t)) return fail(PRISM_EINVAL, "block_norm: tensors must be 16-byte aligned");
-  const NormBwdWs w(p);
-  if (!workspace || ws_bytes < w.total || !aligned16(workspace))
+  const NormBwdShape w(p);
+  const size_t need_ws = (size_t)w.slots * w.groups * 3 * p->channels * 4;
+  if (!workspace || ws_bytes < need_ws || !aligned16(workspace))
     return fail(PRISM_EINVAL, "block_norm: workspace missing, misaligned or below prism_block_norm_workspace_size");
-  uint8_t *ws = static_cast<uint8_t *>(workspace);
-  const bool want = dpost_weight || dgate || dweight || dscale || dshift;
   a.unit = w.unit;
+  a.wpr = w.wpr;
+  a.groups = w.groups;
+  a.stages = w.stages;
   a.y = y;
   a.x_out = const_cast<void *>(x_out);
   a.dh = dh;
   a.dx_out = dx_out;
   a.dx = dx;
   a.dy = dy;
-  a.part = want ? reinterpret_cast<float *>(ws + w.part) : nullptr;
+  a.need = (dweight || dscale ? 1 : 0) | (dshift ? 2 : 0) | (dgate || dpost_weight ? 4 : 0);
+  a.part = static_cast<float *>(workspace);
   cudaStream_t st = as_stream(stream);
   if (p->rows) {
     if (p->stream_dtype == PRISM_BF16)
@@ -426,15 +468,15 @@ int prism_block_norm_bwd(const prism_norm_params *p, const void *x_out, const vo
                                          : launch_norm_bwd<float, float>(w, a, st);
     if (rc) return rc;
   }
-  if (!want) return PRISM_OK;
+  if (!a.need) return PRISM_OK;
   BnParamArgs q = {};
   q.seq = a.seq;
   q.C = a.C;
   q.unit = w.unit;
-  q.rpc = w.shape.rpc;
+  q.groups = w.groups;
   q.param_f32 = a.param_f32;
+  q.need = a.need;
   q.part = a.part;
-  q.sums = reinterpret_cast<float *>(ws + w.sums);
   q.weight = weight;
   q.post_weight = post_weight;
   q.gate = gate;
@@ -449,9 +491,8 @@ int prism_block_norm_bwd(const prism_norm_params *p, const void *x_out, const vo
   q.per_gate = p->gate_stride != 0;
   q.per_scale = p->scale_stride != 0;
   q.per_shift = p->shift_stride != 0;
-  PRISM_TRACED("block_norm_sums_kernel", st, block_norm_sums_kernel<<<dim3((unsigned)((a.C + 31) / 32), p->seqs), 1024, 0, st>>>(q));
-  if (dweight || dpost_weight || (dscale && !q.per_scale) || (dshift && !q.per_shift) || (dgate && !q.per_gate))
-    PRISM_TRACED("block_norm_params_kernel", st, block_norm_params_kernel<<<(unsigned)((a.C + 127) / 128), 128, 0, st>>>(q));
+  const bool per = (dgate && q.per_gate) || (dscale && q.per_scale) || (dshift && q.per_shift);
+  PRISM_TRACED("block_norm_params_kernel", st, block_norm_params_kernel<<<dim3((unsigned)((a.C + 31) / 32), per ? 1 + p->seqs : 1), kBnParamWarps * 32, 0, st>>>(q));
   return PRISM_OK;
 }
 

@@ -143,7 +143,7 @@ def test_packed_pointers_refused(lib):
     (dict(stream_dtype=2), "dtypes"), (dict(branch_dtype=-1), "dtypes"), (dict(param_dtype=5), "dtypes"),
     (dict(post_norm=3), "post_norm"), (dict(pre_norm=0), "pre_norm"), (dict(eps=-1.0), "eps"),
     (dict(alpha=float("nan")), "alpha"), (dict(gate_stride=32), "parameter strides"), (dict(shift_stride=68), "parameter strides"),
-    (dict(seqs=70000), "65535")])
+    (dict(seqs=70000), "65534")])
 def test_norm_params_refused(lib, bad, what):
     with pytest.raises(P.PrismError, match=what) as e:
         P.prism_block_norm_workspace_size(_np(**bad))
