@@ -85,7 +85,7 @@ struct BnVec8<float> {
   }
 };
 __device__ __forceinline__ float2 both(float x) { return tc::f2(x, x); }
-__device__ __forceinline__ float2 add2(float2 a, float2 b) { return tc::fma2(a, both(1.f), b); }
+using tc::add2;
 
 __device__ __forceinline__ float param_at(const void *p, int64_t i, int f32) {
   return f32 ? static_cast<const float *>(p)[i] : __bfloat162float(static_cast<const __nv_bfloat16 *>(p)[i]);

@@ -6,6 +6,7 @@
 #pragma once
 
 #include "attn_common.cuh"
+#include "tc_common.cuh"
 #include "packed_common.cuh"
 
 namespace prism {

@@ -159,8 +159,8 @@ __global__ void __launch_bounds__(kPbThreads, 1)
     tc::mbar_init(b_kv, 1);
     tc::mbar_init(b_s, 1);
     tc::mbar_init(b_dp, 1);
-    tc::mbar_init(b_p, 256);
-    tc::mbar_init(b_ds, 256);
+    tc::mbar_init(b_p, 8);           // one arrival per elementwise warp
+    tc::mbar_init(b_ds, 8);
     tc::mbar_init(b_qedge, 1);
     tc::mbar_init(b_oedge, 1);
     tc::mbar_init(b_drain, 1);
@@ -362,7 +362,7 @@ __global__ void __launch_bounds__(kPbThreads, 1)
       }
       tc::tmem_st_wait();
       tc::tc_fence_before();
-      tc::mbar_arrive(b_p);
+      warp_arrive(b_p);
       if (!warp_wait(b_dp, (uint32_t)n & 1u, abort, limit)) {
         ok = false;
         break;
@@ -371,7 +371,7 @@ __global__ void __launch_bounds__(kPbThreads, 1)
       form_ds(colDP, colDP, p, [&](int j) { return st[32 + j / 4]; });
       tc::tmem_st_wait();
       tc::tc_fence_before();
-      tc::mbar_arrive(b_ds);
+      warp_arrive(b_ds);
     }
     if (__all_sync(0xffffffffu, ok && !*abort)) {
       if (nsteps > 0) ok = warp_wait(b_drain, 0, abort, limit);
@@ -460,7 +460,7 @@ __global__ void __launch_bounds__(kPbThreads, 1)
       tc::mbar_init(b_s(i), 1);
     }
     tc::mbar_init(b_dp, 1);
-    tc::mbar_init(b_ds, 256);
+    tc::mbar_init(b_ds, 8);
     tc::mbar_init(b_kedge, 1);
     tc::mbar_init(b_vedge, 1);
     tc::mbar_init(b_drain, 1);
@@ -628,7 +628,7 @@ __global__ void __launch_bounds__(kPbThreads, 1)
       form_ds(tDP + lane_off + 64u * half, colS, p, [&](int) { return d4; });
       tc::tmem_st_wait();
       tc::tc_fence_before();
-      tc::mbar_arrive(b_ds);
+      warp_arrive(b_ds);
     }
     if (__all_sync(0xffffffffu, ok && !*abort)) {
       if (nsteps > 0) ok = warp_wait(b_drain, 0, abort, limit);

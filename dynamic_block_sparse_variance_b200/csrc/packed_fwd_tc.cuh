@@ -1,7 +1,7 @@
 // Dense attention forward over packed sequences on the tcgen05 tensor cores.
 //
-// One CTA per (256 flattened query rows, kv head, share of the keys): two
-// 128-row tiles A and B that share every key/value tile.
+// One CTA per (128 or 256 flattened query rows, kv head, share of the keys); with
+// 256, two 128-row tiles A and B share every key/value tile.
 //   S = Q K^T (tensor memory), running maximum m and sum l per row,
 //   P = 2^(scale log2e S - m), O += P V (P as bf16 from tensor memory over S).
 // Warps: 0 TMA producer, 1 MMA issuer and tensor-memory owner, 2-5 and 6-9
@@ -12,6 +12,14 @@
 // map (head_dim, kv head, row).  A key tile that reaches past its sequence's
 // keys holds other rows: their scores are replaced by -inf before they are
 // used, and their values by zeros in shared memory (0 x NaN would not be 0).
+//
+// What bounds it is a tile's chain, not one unit: of about 4000 cycles per pair of
+// 128 x 128 tiles the products take 2048 and the special-function unit's
+// exponentials 2048, and with S, P and O of two tiles in all 512 columns of tensor
+// memory the next S of a tile waits for its P V.  Measured (8 heads of 128, 16384
+// causal rows): 512 us, 1070 TFLOP/s.  Slower: eight softmax warps per tile (527
+// us), three of eight exponentials as polynomials on the FMA pipe (598 us: the
+// products themselves then run at 70% of their rate).
 //
 // With few rows the keys are split over blockIdx.z; a share writes its O in
 // fp32 and its log2-sum-exp, and packed_combine_kernel joins them.
@@ -33,6 +41,13 @@ __device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.a
 // 16 bytes global -> shared, or 16 zero bytes.
 __device__ __forceinline__ void cp_async16_or_zero(uint32_t dst, const void *src, bool have) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(dst), "l"(src), "r"(have ? 16 : 0));
+}
+
+// One arrival for a whole warp, after what all of its lanes did (their tensor-memory
+// stores have been waited for and fenced).
+__device__ __forceinline__ void warp_arrive(uint32_t bar) {
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) tc::mbar_arrive(bar);
 }
 
 // A [128][D] bf16 tile of 128-byte-swizzled atoms of 64 columns.
@@ -67,26 +82,29 @@ struct PackedSplit {
   float *lse2;  // [split][heads][q_rows]
 };
 
-template <int D>
+// NG query tiles of 128 rows: 2, which share each key/value tile, one CTA per SM;
+// or 1, two CTAs per SM, whose fixed costs (Q, the first tiles, the epilogue)
+// overlap each other's work.
+template <int D, int NG>
 struct PfCfg {
-  static constexpr int kStages = D == 128 ? 2 : 4;
-  static constexpr int kSmem = Tile<D>::kBytes * (2 + 2 * kStages) + 512 + 1024;
+  static constexpr int kStages = (D == 128 ? 1 : 2) * NG;
+  static constexpr int kThreads = 64 + 128 * NG;
+  static constexpr int kSmem = Tile<D>::kBytes * (NG + 2 * kStages) + 512 + 1024;
 };
-constexpr int kPfThreads = 320;
 
-template <int D>
-__global__ void __launch_bounds__(kPfThreads, 1)
+template <int D, int NG>
+__global__ void __launch_bounds__(64 + 128 * NG, 3 - NG)
     packed_fwd_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                          const PackedArgs a, const PackedSplit sp, const uint32_t limit) {
   using T = Tile<D>;
-  constexpr int kStages = PfCfg<D>::kStages;
+  constexpr int kStages = PfCfg<D, NG>::kStages, kThreads = PfCfg<D, NG>::kThreads;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t sbase = (smem_u32(smem_raw) + 1023u) & ~1023u;
   uint8_t *sgen = smem_raw + (sbase - smem_u32(smem_raw));
   auto sQ = [&](int g) { return sbase + (uint32_t)g * T::kBytes; };
-  auto sK = [&](int s) { return sbase + (uint32_t)(2 + 2 * s) * T::kBytes; };
-  auto sV = [&](int s) { return sbase + (uint32_t)(3 + 2 * s) * T::kBytes; };
-  const uint32_t sBar = sbase + (uint32_t)(2 + 2 * kStages) * T::kBytes;
+  auto sK = [&](int s) { return sbase + (uint32_t)(NG + 2 * s) * T::kBytes; };
+  auto sV = [&](int s) { return sbase + (uint32_t)(NG + 1 + 2 * s) * T::kBytes; };
+  const uint32_t sBar = sbase + (uint32_t)(NG + 2 * kStages) * T::kBytes;
   auto b_kfull = [&](int s) { return sBar + 8u * s; };
   auto b_vfull = [&](int s) { return sBar + 8u * (4 + s); };
   auto b_kempty = [&](int s) { return sBar + 8u * (8 + s); };
@@ -104,29 +122,29 @@ __global__ void __launch_bounds__(kPfThreads, 1)
   const int kvh = (int)(blockIdx.x % a.kv_heads), slot = slots - 1 - (int)(blockIdx.x / a.kv_heads);
   PackedSeq::check(a, slot);
   int64_t piece;
-  const int b = find_sequence(a.qs, slot, a.group, 256, piece);
+  const int b = find_sequence(a.qs, slot, a.group, 128 * NG, piece);
   PackedSeq s;
   if (!s.load(a, b)) return;
   const int64_t nrows = (int64_t)s.lq * a.group;
-  if (piece < 0 || piece * 256 >= nrows) return;
-  const int r0 = (int)(piece * 256);                   // first flattened row
-  const int rows = (int)min((int64_t)256, nrows - r0);
+  if (piece < 0 || piece * (128 * NG) >= nrows) return;
+  const int r0 = (int)(piece * (128 * NG));            // first flattened row
+  const int rows = (int)min((int64_t)(128 * NG), nrows - r0);
   // key tiles [t0, t1[g]) of tile g
-  int t0, t1[2];
+  int t0, t1[NG];
   {
-    int top[2];
+    int top[NG];
 #pragma unroll
-    for (int g = 0; g < 2; ++g) {
+    for (int g = 0; g < NG; ++g) {
       const int last = min(rows, 128 * (g + 1)) - 1;    // tile g's last row
       top[g] = last >= 128 * g ? (s.visible(a, (r0 + last) / a.group) + 127) >> 7 : 0;
     }
-    const int all = max(top[0], top[1]);
+    const int all = max(top[0], top[NG - 1]);
     t0 = (int)((int64_t)all * blockIdx.z / sp.splits);
     const int te = (int)((int64_t)all * (blockIdx.z + 1) / sp.splits);
-    t1[0] = max(t0, min(te, top[0]));
-    t1[1] = max(t0, min(te, top[1]));
+#pragma unroll
+    for (int g = 0; g < NG; ++g) t1[g] = max(t0, min(te, top[g]));
   }
-  const int tend = max(t1[0], t1[1]);
+  const int tend = max(t1[0], t1[NG - 1]);
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < kStages; ++i) {
@@ -135,9 +153,9 @@ __global__ void __launch_bounds__(kPfThreads, 1)
       tc::mbar_init(b_kempty(i), 1);
       tc::mbar_init(b_vempty(i), 1);
     }
-    for (int g = 0; g < 2; ++g) {
+    for (int g = 0; g < NG; ++g) {
       tc::mbar_init(b_sfull(g), 1);
-      tc::mbar_init(b_pfull(g), 128);
+      tc::mbar_init(b_pfull(g), 4);      // one arrival per warp
     }
     tc::mbar_init(b_edge, 1);
     tc::mbar_init(b_drain, 1);
@@ -145,11 +163,11 @@ __global__ void __launch_bounds__(kPfThreads, 1)
     tc::fence_barrier_init();
   }
   if (warp == 1) {
-    tc::tmem_alloc(smem_u32(tmem_slot), 512);
+    tc::tmem_alloc(smem_u32(tmem_slot), 256 * NG);
     tc::tmem_relinquish();
   }
   // Q: flattened row r0 + r is token (r0 + r) / group, head kvh group + (r0 + r) % group
-  for (int i = threadIdx.x; i < 256 * (D / 8); i += kPfThreads) {
+  for (int i = threadIdx.x; i < 128 * NG * (D / 8); i += kThreads) {
     const int r = i / (D / 8), ch = i % (D / 8);
     const bool have = r < rows;
     const int fr = r0 + (have ? r : 0), tok = fr / a.group;
@@ -218,8 +236,8 @@ __global__ void __launch_bounds__(kPfThreads, 1)
     if (lane == 0) {
       constexpr uint32_t idS = tc::idesc_bf16(128, 128, false, false);
       constexpr uint32_t idO = tc::idesc_bf16(128, D, false, true);
-      const int n_all = tend - t0, n_g[2] = {t1[0] - t0, t1[1] - t0};
-      const uint64_t dQ[2] = {tc::sw128_desc(sQ(0), 16, 1024), tc::sw128_desc(sQ(1), 16, 1024)};
+      const int n_all = tend - t0, n_g[2] = {t1[0] - t0, t1[NG - 1] - t0};
+      const uint64_t dQ[2] = {tc::sw128_desc(sQ(0), 16, 1024), tc::sw128_desc(sQ(NG - 1), 16, 1024)};
       auto issue_s = [&](int n, int g) {
         const uint64_t dK = tc::sw128_desc(sK(n % kStages), 16, 1024), dQg = dQ[g];
         const uint32_t tSg = tS(g);
@@ -244,29 +262,28 @@ __global__ void __launch_bounds__(kPfThreads, 1)
       // runs while the other tile's products execute
       bool ok = n_all == 0 || wait_full(b_kfull(0), 0);
       if (ok && n_all > 0) {
-        for (int g = 0; g < 2; ++g)
+        for (int g = 0; g < NG; ++g)
           if (n_g[g] > 0) issue_s(0, g);
         tc::mma_commit(b_kempty(0));
       }
       for (int n = 0; ok && n < n_all; ++n) {
         const int st = n % kStages;
         const bool more = n + 1 < n_all;
-        bool have_v = false, have_k = false;
-        for (int g = 0; g < 2 && ok; ++g) {
+        bool have_k = false;
+        if (!wait_full(b_vfull(st), n)) break;
+        for (int g = 0; g < NG && ok; ++g) {
           if (n < n_g[g]) {
             if (!tc::mbar_wait(b_pfull(g), (uint32_t)n & 1u, abort, limit)) { ok = false; break; }
-            if (!have_v && !wait_full(b_vfull(st), n)) { ok = false; break; }
-            have_v = true;
             tc::tc_fence_after();
             issue_pv(n, g);
           }
-          if (g == 1) tc::mma_commit(b_vempty(st));
+          if (g == NG - 1) tc::mma_commit(b_vempty(st));
           if (n + 1 < n_g[g]) {
             if (!have_k && !wait_full(b_kfull((n + 1) % kStages), n + 1)) { ok = false; break; }
             have_k = true;
             issue_s(n + 1, g);
           }
-          if (g == 1 && more) tc::mma_commit(b_kempty((n + 1) % kStages));
+          if (g == NG - 1 && more) tc::mma_commit(b_kempty((n + 1) % kStages));
         }
       }
       tc::mma_commit(b_drain);
@@ -277,7 +294,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
     // ------------------------------------------------------------ softmax
     const int g = (warp - 2) >> 2;
     const int q = warp & 3;                      // tensor-memory lane quadrant
-    const int row = 128 * g + 32 * q + lane;     // of the CTA's 256
+    const int row = 128 * g + 32 * q + lane;     // of the CTA's rows
     const uint32_t lane_off = (uint32_t)(32 * q) << 16;
     const bool have = row < rows;
     const int fr = r0 + row, tok = have ? fr / a.group : 0;
@@ -356,7 +373,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
       l_run += ((r2[0].x + r2[0].y) + (r2[1].x + r2[1].y)) + ((r2[2].x + r2[2].y) + (r2[3].x + r2[3].y));
       tc::tmem_st_wait();
       tc::tc_fence_before();
-      tc::mbar_arrive(b_pfull(g));
+      warp_arrive(b_pfull(g));
     }
     // epilogue
     if (__all_sync(0xffffffffu, ok && !*abort)) {
@@ -417,7 +434,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
   __syncthreads();
   if (warp == 1) {
     tc::tc_fence_after();
-    tc::tmem_dealloc(tmem, 512);
+    tc::tmem_dealloc(tmem, 256 * NG);
   }
 }
 
@@ -437,14 +454,14 @@ __global__ void __launch_bounds__(256) packed_combine_kernel(const PackedArgs a,
   const float *L = sp.lse2 + (int64_t)h * a.qs.rows + row;
   const int64_t ls = (int64_t)a.heads * a.qs.rows;
   float m = -INFINITY;
+#pragma unroll 4
   for (int s = 0; s < sp.splits; ++s) m = fmaxf(m, L[s * ls]);
   float l = 0.f;
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
   if (m > -INFINITY) {
+#pragma unroll 4
     for (int s = 0; s < sp.splits; ++s) {
-      const float x = L[s * ls];
-      if (x == -INFINITY) continue;        // an empty share wrote no O worth reading
-      const float w = exp2f(x - m);
+      const float w = exp2f(L[s * ls] - m);       // 0 for a share without keys, whose O is 0
       const float4 p = *reinterpret_cast<const float4 *>(sp.o + (s * (int64_t)a.qs.rows * a.heads + i) * D + sub * 4);
       l += w;
       o.x = fmaf(w, p.x, o.x); o.y = fmaf(w, p.y, o.y); o.z = fmaf(w, p.z, o.z); o.w = fmaf(w, p.w, o.w);

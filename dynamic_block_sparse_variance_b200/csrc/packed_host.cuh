@@ -4,6 +4,7 @@
 
 #include "block_norm.cuh"
 #include "packed_bwd_tc.cuh"
+#include "packed_fwd_rows.cuh"
 
 namespace prism {
 
@@ -98,17 +99,22 @@ static bool make_head_map(CUtensorMap *map, const void *base, int D, int heads, 
 
 static uint32_t wait_limit() { return g_wait_limit ? g_wait_limit : kDefaultWaitLimit; }
 
-// How the forward's keys are split: over about as many CTAs as there are SMs
-// when the query rows alone give fewer, with at least 512 keys a share.  The
-// host knows the rows, not the sequences' lengths, and goes by their average.
+// Which forward kernel runs and how the keys are split.  The host knows the rows,
+// not the sequences' lengths, and goes by their average; either kernel is right for
+// any.  Up to 16 flattened rows per sequence: the 16-row kernel.  Keys are split when
+// the query rows alone give fewer CTAs than the SMs take (two of the 16-row
+// kernel's waves, one of the others), in shares of at least 128 or 512 keys.
 struct PackedFwdWs {
+  bool few;
   int splits;
   size_t o, lse2, total;
   explicit PackedFwdWs(const prism_packed_params *p) {
     const int64_t group = p->heads / p->kv_heads;
+    few = p->q_rows * group <= (int64_t)16 * p->seqs;
     const int64_t ctas = std::max<int64_t>(1, std::max<int64_t>(p->seqs, p->q_rows * group / 256) * p->kv_heads);
     const int64_t keys = p->k_rows / p->seqs;
-    splits = (int)std::max<int64_t>(1, std::min<int64_t>({148 / ctas, keys / 512, 64}));
+    splits = (int)std::max<int64_t>(1, few ? std::min<int64_t>({(296 + ctas - 1) / ctas, keys / 128, 64})
+                                           : std::min<int64_t>({148 / ctas, keys / 512, 64}));
     const size_t n = (size_t)p->q_rows * p->heads;
     o = 0;
     lse2 = splits > 1 ? align256(n * splits * p->head_dim * 4) : 0;
@@ -117,9 +123,16 @@ struct PackedFwdWs {
 };
 
 template <int D>
-static int launch_packed_fwd(const prism_packed_params *p, const PackedArgs &a, uint8_t *ws, cudaStream_t st) {
-  const PackedFwdWs w(p);
-  PackedSplit sp{w.splits, reinterpret_cast<float *>(ws + w.o), reinterpret_cast<float *>(ws + w.lse2)};
+static int launch_packed_fwd_rows(const prism_packed_params *p, const PackedArgs &a, const PackedSplit &sp, cudaStream_t st) {
+  cudaFuncSetAttribute(packed_fwd_rows_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, kPrSmem<D>);
+  const int64_t grid = slot_bound(p->q_rows, p->seqs, a.group, 16) * a.kv_heads;
+  if (grid > 0x7fffffffLL) return fail(PRISM_EINVAL, "packed: too many query rows");
+  PRISM_TRACED("packed_fwd_rows_kernel", st, packed_fwd_rows_kernel<D><<<dim3((unsigned)grid, 1, sp.splits), kPrWarps * 32, kPrSmem<D>, st>>>(a, sp));
+  return PRISM_OK;
+}
+
+template <int D, int NG>
+static int launch_packed_fwd_tc(const prism_packed_params *p, const PackedArgs &a, const PackedSplit &sp, cudaStream_t st) {
   CUtensorMap tk, tv;
   // without keys nothing is loaded: the maps then only need to be well formed
   const bool keys = p->k_rows > 0;
@@ -127,11 +140,23 @@ static int launch_packed_fwd(const prism_packed_params *p, const PackedArgs &a, 
   if (!make_head_map(&tk, keys ? (const void *)a.k : a.q, D, keys ? a.kv_heads : 1, keys ? p->k_rows : 1, keys ? a.sk : dummy) ||
       !make_head_map(&tv, keys ? (const void *)a.v : a.q, D, keys ? a.kv_heads : 1, keys ? p->k_rows : 1, keys ? a.sv : dummy))
     return fail(PRISM_ECUDA, "cuTensorMapEncodeTiled failed");
-  cudaFuncSetAttribute(packed_fwd_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, PfCfg<D>::kSmem);
-  const int64_t slots = slot_bound(p->q_rows, p->seqs, a.group, 256);
+  using Cfg = PfCfg<D, NG>;
+  cudaFuncSetAttribute(packed_fwd_tc_kernel<D, NG>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::kSmem);
+  const int64_t slots = slot_bound(p->q_rows, p->seqs, a.group, 128 * NG);
   if (slots * a.kv_heads > 0x7fffffffLL) return fail(PRISM_EINVAL, "packed: too many query rows");
-  const dim3 grid((unsigned)(slots * a.kv_heads), 1, w.splits);
-  PRISM_TRACED("packed_fwd_tc_kernel", st, packed_fwd_tc_kernel<D><<<grid, kPfThreads, PfCfg<D>::kSmem, st>>>(tk, tv, a, sp, wait_limit()));
+  const dim3 grid((unsigned)(slots * a.kv_heads), 1, sp.splits);
+  PRISM_TRACED("packed_fwd_tc_kernel", st, packed_fwd_tc_kernel<D, NG><<<grid, Cfg::kThreads, Cfg::kSmem, st>>>(tk, tv, a, sp, wait_limit()));
+  return PRISM_OK;
+}
+
+template <int D>
+static int launch_packed_fwd(const prism_packed_params *p, const PackedArgs &a, uint8_t *ws, cudaStream_t st) {
+  const PackedFwdWs w(p);
+  PackedSplit sp{w.splits, reinterpret_cast<float *>(ws + w.o), reinterpret_cast<float *>(ws + w.lse2)};
+  // Pairs of tiles from 512 keys per sequence on, single tiles below: 8192 keys 299
+  // against 313 us, 910 keys 110 against 115, 278 keys 38 against 34 us.
+  const int rc = w.few ? launch_packed_fwd_rows<D>(p, a, sp, st) : p->k_rows / p->seqs < 512 ? launch_packed_fwd_tc<D, 1>(p, a, sp, st) : launch_packed_fwd_tc<D, 2>(p, a, sp, st);
+  if (rc) return rc;
   if (w.splits > 1) {
     const int64_t threads = p->q_rows * p->heads * (D / 4);
     PRISM_TRACED("packed_combine_kernel", st, packed_combine_kernel<D><<<(unsigned)((threads + 255) / 256), 256, 0, st>>>(a, sp));
