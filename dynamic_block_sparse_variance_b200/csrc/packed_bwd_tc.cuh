@@ -100,11 +100,10 @@ __device__ __forceinline__ void store_row(uint32_t taddr, bool have, bool zero, 
   }
 }
 
+// The kind that keeps dK and dV; `block`: its number among the CTAs of its kind.
 template <int D>
-__global__ void __launch_bounds__(kPbThreads, 1)
-    packed_dkdv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
-                          const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmO,
-                          const PackedArgs a, const uint32_t limit) {
+__device__ __forceinline__ void packed_keys_cta(const CUtensorMap &tmQ, const CUtensorMap &tmK, const CUtensorMap &tmV,
+                                                const CUtensorMap &tmO, const PackedArgs &a, const uint32_t limit, int block) {
   using T = Tile<D>;
   extern __shared__ __align__(1024) uint8_t sgen[];
   const uint32_t sbase = smem_u32(sgen);
@@ -133,7 +132,7 @@ __global__ void __launch_bounds__(kPbThreads, 1)
   volatile int *abort = reinterpret_cast<volatile int *>(sgen + (sBar - sbase) + 8 * 20 + 4);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int kvh = (int)(blockIdx.x % a.kv_heads), slot = (int)(blockIdx.x / a.kv_heads);
+  const int kvh = block % a.kv_heads, slot = block / a.kv_heads;
   int64_t piece;
   const int b = find_sequence(a.ks, slot, 1, 128, piece);
   PackedSeq s;
@@ -288,20 +287,17 @@ __global__ void __launch_bounds__(kPbThreads, 1)
       for (int n = 0; ok && n < nsteps; ++n) {
         const int m = n + 1;
         const bool more = m < nsteps;
+        // the copies were asked for long ago: seeing here that they landed keeps it off the
+        // way from P and dS to their products
+        if (more && !(wait(b_qfull(m % 3), (uint32_t)(m / 3) & 1u) && wait(b_ofull(m & 1), (uint32_t)(m >> 1) & 1u))) break;
         if (!wait(b_p, (uint32_t)n & 1u)) break;
         accumulate(tdV, tS, sO(n & 1), n > 0);
         tc::mma_commit(b_oempty(n & 1));
-        if (more) {
-          if (!wait(b_qfull(m % 3), (uint32_t)(m / 3) & 1u)) break;
-          rows_by_rows(tS, dK, sQ(m % 3), b_s);
-        }
+        if (more) rows_by_rows(tS, dK, sQ(m % 3), b_s);
         if (!wait(b_ds, (uint32_t)n & 1u)) break;
         accumulate(tdK, tDP, sQ(n % 3), n > 0);
         tc::mma_commit(b_qempty(n % 3));
-        if (more) {
-          if (!wait(b_ofull(m & 1), (uint32_t)(m >> 1) & 1u)) break;
-          rows_by_rows(tDP, dV, sO(m & 1), b_dp);
-        }
+        if (more) rows_by_rows(tDP, dV, sO(m & 1), b_dp);
       }
       tc::mma_commit(b_drain);
       volatile int no_abort = 0;
@@ -407,10 +403,10 @@ __global__ void __launch_bounds__(kPbThreads, 1)
   }
 }
 
+// The kind that keeps dQ, `block` of `blocks`.
 template <int D>
-__global__ void __launch_bounds__(kPbThreads, 1)
-    packed_dq_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
-                        const PackedArgs a, const uint32_t limit) {
+__device__ __forceinline__ void packed_queries_cta(const CUtensorMap &tmK, const CUtensorMap &tmV, const PackedArgs &a,
+                                                   const uint32_t limit, int block, int blocks) {
   using T = Tile<D>;
   extern __shared__ __align__(1024) uint8_t sgen[];
   const uint32_t sbase = smem_u32(sgen);
@@ -436,8 +432,7 @@ __global__ void __launch_bounds__(kPbThreads, 1)
   volatile int *abort = reinterpret_cast<volatile int *>(sgen + (sBar - sbase) + 8 * 20 + 4);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int slots = (int)(gridDim.x / a.kv_heads);
-  const int kvh = (int)(blockIdx.x % a.kv_heads), slot = slots - 1 - (int)(blockIdx.x / a.kv_heads);
+  const int kvh = block % a.kv_heads, slot = blocks / a.kv_heads - 1 - block / a.kv_heads;   // long ones first
   PackedSeq::check(a, slot);
   int64_t piece;
   const int b = find_sequence(a.qs, slot, a.group, 128, piece);
@@ -559,16 +554,20 @@ __global__ void __launch_bounds__(kPbThreads, 1)
         rows_by_rows(tS(n & 1), dQ, sK(n % 3), b_s(n & 1));
         return true;
       };
+      auto landed_v = [&](int n) { return wait(b_vfull(n & 1), (uint32_t)(n >> 1) & 1u); };
       auto dprob = [&](int n) {
-        if (!wait(b_vfull(n & 1), (uint32_t)(n >> 1) & 1u)) return false;
         rows_by_rows(tDP, dO, sV(n & 1), b_dp);
         tc::mma_commit(b_vempty(n & 1));
-        return true;
       };
-      bool ok = scores(0) && dprob(0) && (nsteps < 2 || scores(1));
+      bool ok = scores(0) && landed_v(0);
+      if (ok) {
+        dprob(0);
+        ok = nsteps < 2 || scores(1);
+      }
       for (int n = 0; ok && n < nsteps; ++n) {
+        if (n + 1 < nsteps && !landed_v(n + 1)) break;
         if (!wait(b_ds, (uint32_t)n & 1u)) break;
-        if (n + 1 < nsteps && !dprob(n + 1)) break;
+        if (n + 1 < nsteps) dprob(n + 1);
         const uint64_t y = tc::sw128_desc(sK(n % 3), T::kAtom, 1024);
 #pragma unroll
         for (int k = 0; k < 8; ++k)
@@ -646,6 +645,19 @@ __global__ void __launch_bounds__(kPbThreads, 1)
     tc::tc_fence_after();
     tc::tmem_dealloc(tmem, 512);
   }
+}
+
+// Both kinds in one launch: the first `key_blocks` CTAs keep dK and dV (their loops
+// are longer), the others dQ, which fill the SMs as the first kind runs out (8192
+// tokens, 8 heads: 512 CTAs of either kind on 148 SMs).
+template <int D>
+__global__ void __launch_bounds__(kPbThreads, 1)
+    packed_bwd_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                         const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmO,
+                         const PackedArgs a, const uint32_t limit, const int key_blocks) {
+  const int block = (int)blockIdx.x;
+  if (block < key_blocks) packed_keys_cta<D>(tmQ, tmK, tmV, tmO, a, limit, block);
+  else packed_queries_cta<D>(tmK, tmV, a, limit, block - key_blocks, (int)gridDim.x - key_blocks);
 }
 
 }  // namespace prism

@@ -181,18 +181,12 @@ static int launch_packed_bwd(const prism_packed_params *p, const PackedArgs &a, 
     const int64_t threads = p->q_rows * p->heads * (D / 4);
     PRISM_TRACED("packed_stats_kernel", st, packed_stats_kernel<D><<<(unsigned)((threads + 255) / 256), 256, 0, st>>>(a, a.o, delta, lse2));
   }
-  if (keys) {
-    const int64_t grid = slot_bound(p->k_rows, p->seqs, 1, 128) * a.kv_heads;
-    if (grid > 0x7fffffffLL) return fail(PRISM_EINVAL, "packed: too many key rows");
-    cudaFuncSetAttribute(packed_dkdv_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, kPbSmem<D>);
-    PRISM_TRACED("packed_dkdv_tc_kernel", st, packed_dkdv_tc_kernel<D><<<(unsigned)grid, kPbThreads, kPbSmem<D>, st>>>(tq, tk, tv, to, a, wait_limit()));
-  }
-  if (rows) {
-    const int64_t grid = slot_bound(p->q_rows, p->seqs, a.group, 128) * a.kv_heads;
-    if (grid > 0x7fffffffLL) return fail(PRISM_EINVAL, "packed: too many query rows");
-    cudaFuncSetAttribute(packed_dq_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, kPbSmem<D>);
-    PRISM_TRACED("packed_dq_tc_kernel", st, packed_dq_tc_kernel<D><<<(unsigned)grid, kPbThreads, kPbSmem<D>, st>>>(tk, tv, a, wait_limit()));
-  }
+  const int64_t key_blocks = keys ? slot_bound(p->k_rows, p->seqs, 1, 128) * a.kv_heads : 0;
+  const int64_t blocks = key_blocks + (rows ? slot_bound(p->q_rows, p->seqs, a.group, 128) * a.kv_heads : 0);
+  if (blocks > 0x7fffffffLL) return fail(PRISM_EINVAL, "packed: too many rows");
+  if (blocks == 0) return PRISM_OK;
+  cudaFuncSetAttribute(packed_bwd_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, kPbSmem<D>);
+  PRISM_TRACED("packed_bwd_tc_kernel", st, packed_bwd_tc_kernel<D><<<(unsigned)blocks, kPbThreads, kPbSmem<D>, st>>>(tq, tk, tv, to, a, wait_limit(), (int)key_blocks));
   return PRISM_OK;
 }
 

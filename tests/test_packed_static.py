@@ -11,7 +11,8 @@ SOURCES = sorted(p.name for p in CSRC.glob("packed_*_tc.cuh"))
 
 
 def _kernels(text):
-    starts = [m.start() for m in re.finditer(r"__global__ void", text)]
+    """Texts of the kernels and of the device functions that are a CTA's whole work."""
+    starts = [m.start() for m in re.finditer(r"__global__ void|void packed_\w+_cta\(", text)]
     for a, b in zip(starts, starts[1:] + [len(text)]):
         yield text[a:b]
 
