@@ -200,9 +200,14 @@ __device__ __forceinline__ void packed_keys_cta(const CUtensorMap &tmQ, const CU
       const int valid = min(tt, s.lq - tok) * a.group;     // rows of the tile
       const bool last = s.lq - tok < tt;
       const int qi = n % 3, oi = n & 1;
+      // both copies first: what follows (rows of LSE and D, the last tile's zeros) waits
+      // for more
       if (!warp_wait(b_qempty(qi), ((uint32_t)(n / 3) & 1u) ^ 1u, abort, limit)) break;
       if (lane == 0) fetch(sQ(qi), &tmQ, tok, last ? b_qedge : b_qfull(qi));
       (last ? qedge : nq) += 1;
+      if (!warp_wait(b_oempty(oi), ((uint32_t)(n >> 1) & 1u) ^ 1u, abort, limit)) break;
+      if (lane == 0) fetch(sO(oi), &tmO, tok, last ? b_oedge : b_ofull(oi));
+      (last ? oedge : no) += 1;
       {
         const int64_t r = (int64_t)(s.q0 + tok) * a.group;
         float L[4], Dr[4];
@@ -224,23 +229,16 @@ __device__ __forceinline__ void packed_keys_cta(const CUtensorMap &tmQ, const CU
       if (last) {
         if (!warp_wait(b_qedge, 0, abort, limit)) break;
         T::zero_rows(sgen + (sQ(qi) - sbase), valid);
-        fence_async_smem();
-        __syncwarp();
-        if (lane == 0) tc::mbar_arrive(b_qfull(qi));
-      }
-      tc::mbar_arrive(b_qfull(qi));
-      if (!warp_wait(b_oempty(oi), ((uint32_t)(n >> 1) & 1u) ^ 1u, abort, limit)) break;
-      if (lane == 0) fetch(sO(oi), &tmO, tok, last ? b_oedge : b_ofull(oi));
-      if (last) {
-        oedge = 1;
         if (!warp_wait(b_oedge, 0, abort, limit)) break;
         T::zero_rows(sgen + (sO(oi) - sbase), valid);
         fence_async_smem();
         __syncwarp();
-        if (lane == 0) tc::mbar_arrive(b_ofull(oi));
-      } else {
-        ++no;
+        if (lane == 0) {
+          tc::mbar_arrive(b_qfull(qi));
+          tc::mbar_arrive(b_ofull(oi));
+        }
       }
+      tc::mbar_arrive(b_qfull(qi));
     }
     // Every copy lands before the CTA exits (the last tile took the stage of the
     // oldest fill, which had been read; each remaining parity is unambiguous).
