@@ -30,6 +30,11 @@ def _need(ok, msg):
         raise P.PrismError(P.PRISM_EINVAL, msg)
 
 
+def _like(t):
+    """A new contiguous tensor of t's shape and type (empty_like keeps the order of strides of a dense t)."""
+    return torch.empty_like(t) if t.is_contiguous() else t.new_empty(t.shape)
+
+
 _plans = {}
 
 
@@ -44,17 +49,18 @@ def _plan(key, make):
     return p
 
 
-def _same_device(index, **tensors):
-    for name, t in tensors.items():
-        _need(t is None or t.get_device() == index, f"{name} is not on device {index}")
+def _same_device(index, *tensors):
+    for t in tensors:
+        if t is not None and t.get_device() != index:
+            raise P.PrismError(P.PRISM_EINVAL, f"all tensors must be on device {index}, one is on {t.device}")
 
 
 def _index(t, index, name):
     """A device array of int32: offsets or lengths. Its number of entries (-1: none)."""
     if t is None:
         return -1
-    _need(t.dtype == torch.int32 and t.dim() == 1 and t.is_contiguous() and t.get_device() == index,
-          f"{name} must be a contiguous int32 vector on device {index}")
+    if not (t.dtype is torch.int32 and t.dim() == 1 and t.is_contiguous() and t.get_device() == index):
+        raise P.PrismError(P.PRISM_EINVAL, f"{name} must be a contiguous int32 vector on device {index}")
     return t.shape[0]
 
 
@@ -141,8 +147,7 @@ class PackedAttention:
                 return self.forward(q, k, v, q_offsets, k_offsets, k_used=k_used, out=out)
         if not (q.dtype is _BF16 and k.dtype is _BF16 and v.dtype is _BF16 and (out is None or out.dtype is _BF16)):
             raise TypeError("q, k, v and out must be bfloat16")
-        if not (k.get_device() == at and v.get_device() == at and (out is None or out.get_device() == at)):
-            _same_device(at, k=k, v=v, out=out)
+        _same_device(at, k, v, out)
         if k_offsets is None and k.dim() == 3:
             k_offsets = q_offsets
         n_qo, n_used = _index(q_offsets, at, "q_offsets"), _index(k_used, at, "k_used")
@@ -158,10 +163,10 @@ class PackedAttention:
         if not plan.offsets:
             q_offsets = k_offsets = k_used = None
         if out is None:
-            out = torch.empty(q.shape, dtype=_BF16, device=q.device)
-        lse = torch.empty((self.heads, plan.q_rows), dtype=torch.float32, device=q.device)
-        o_res = torch.empty((plan.q_rows, self.heads, self.head_dim), dtype=_BF16, device=q.device) if self.training else None
-        ws = torch.empty(plan.ws, dtype=torch.uint8, device=q.device) if plan.ws else None
+            out = _like(q)
+        lse = q.new_empty((self.heads, plan.q_rows), dtype=torch.float32)
+        o_res = q.new_empty((plan.q_rows, self.heads, self.head_dim)) if self.training else None
+        ws = q.new_empty(plan.ws, dtype=torch.uint8) if plan.ws else None
         P.prism_packed_attn_fwd(plan.p, q, k, v, q_offsets, k_offsets, k_used, out, o_res, lse, ws, _raw_stream(at))
         self.lse = lse
         self._saved = (key, plan.p, q, k, v, out, o_res, lse, q_offsets, k_offsets, k_used) if self.training else None
@@ -184,7 +189,7 @@ class PackedAttention:
             with torch.cuda.device(at):
                 return self.backward(dout, dq, dk, dv)
         _need(dout.shape == q.shape, "dout must have the shape of q")
-        _same_device(at, dout=dout, dq=dq, dk=dk, dv=dv)
+        _same_device(at, dout, dq, dk, dv)
         strides = [dout.stride()]
         for name, g, like in (("dq", dq, q), ("dk", dk, k), ("dv", dv, v)):
             _need(g is None or g.shape == like.shape, f"{name} must have the shape of its input")
@@ -193,9 +198,10 @@ class PackedAttention:
             if g is not None and g.dtype is not _BF16:
                 raise TypeError("dout, dq, dk and dv must be bfloat16")
         bp, n = _plan((key, *strides), lambda: self._backward_plan(p, (q.shape, q.shape, k.shape, v.shape), strides))
-        dq, dk, dv = (torch.empty(like.shape, dtype=_BF16, device=q.device) if g is None else g
-                      for g, like in ((dq, q), (dk, k), (dv, v)))
-        ws = torch.empty(n, dtype=torch.uint8, device=q.device) if n else None
+        dq = _like(q) if dq is None else dq
+        dk = _like(k) if dk is None else dk
+        dv = _like(v) if dv is None else dv
+        ws = q.new_empty(n, dtype=torch.uint8) if n else None
         P.prism_packed_attn_bwd(bp, q, k, v, o, o_res, dout, lse, q_offsets, k_offsets, k_used, dq, dk, dv, ws,
                                 _raw_stream(at))
         return dq, dk, dv
@@ -306,18 +312,18 @@ class BlockNorm:
                 return self.forward(x, y, offsets=offsets, post_weight=post_weight, gate=gate, weight=weight, scale=scale,
                                     shift=shift, x_out=x_out, h=h, y_norms=y_norms, h_dtype=h_dtype)
         params = (post_weight, gate, weight, scale, shift)
-        for t in (y, x_out, h, y_norms) + params:
-            _need(t is None or t.get_device() == at, f"all tensors must be on device {at}")
+        _same_device(at, y, x_out, h, y_norms, *params)
         n_off = _index(offsets, at, "offsets")
         if y is None:
             x_out = None
-        layouts = (_layout(x), _layout(y), _layout(x_out), _layout(h), h_dtype, n_off, tuple(_layout(t) for t in params))
+        layouts = (_layout(x), _layout(y), _layout(x_out), _layout(h), h_dtype, n_off,
+                   (_layout(post_weight), _layout(gate), _layout(weight), _layout(scale), _layout(shift)))
         key = (self.channels, self.post, self.pre, self.eps, self.alpha, layouts)
         plan = _plan(key, lambda: self._forward_plan(*layouts))
         if y is not None and x_out is None:
-            x_out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+            x_out = _like(x)
         if h is None:
-            h = torch.empty(x.shape, dtype=plan.branch, device=x.device)
+            h = _like(x) if plan.branch is x.dtype else x.new_empty(x.shape, dtype=plan.branch)
         if y_norms is not None:
             _need(y_norms.dtype == torch.float32 and y_norms.is_contiguous() and y_norms.numel() == plan.p.rows,
                   f"y_norms must be {plan.p.rows} contiguous floats")
@@ -349,19 +355,18 @@ class BlockNorm:
         if at != torch.cuda.current_device():
             with torch.cuda.device(at):
                 return self.backward(dh, dx_out, dx, dy)
-        _same_device(at, dh=dh, dx_out=dx_out, dx=dx, dy=dy)
+        _same_device(at, dh, dx_out, dx, dy)
         given = (_layout(dh), _layout(dx_out), _layout(dx), None if y is None else _layout(dy))
         p = _plan((key, given), lambda: self._backward_plan(plan, kept.shape, y, given))
         if dx is None:
-            dx = torch.empty(kept.shape, dtype=kept.dtype, device=kept.device)
+            dx = _like(kept)
         if y is None:
             dy = None
         elif dy is None:
-            dy = torch.empty(y.shape, dtype=y.dtype, device=y.device)
+            dy = _like(y)
         post_weight, gate, weight, scale, shift = params
-        grads = [None if t is None or (y is None and i < 2) else torch.empty(t.shape, dtype=t.dtype, device=t.device)
-                 for i, t in enumerate(params)]
-        ws = torch.empty(plan.ws, dtype=torch.uint8, device=kept.device)
+        grads = [None if t is None or (y is None and i < 2) else _like(t) for i, t in enumerate(params)]
+        ws = kept.new_empty(plan.ws, dtype=torch.uint8)
         P.prism_block_norm_bwd(p, kept, y, offsets, post_weight, gate, weight, scale, dh, dx_out, dx, dy, *grads, ws,
                                _raw_stream(at))
         return {"dx": dx, "dy": dy, **{"d" + n: g for n, g in zip(_PARAMS, grads)}}
