@@ -380,6 +380,10 @@ struct BnGroup {
   uint32_t ring_addr, bars;
   float *red;                          // [2][wpr][8]
   int buf, st_get, st_put, ph;         // stage to read and its phase, stage to fill
+  bool issues;                         // this thread issues a copy per batch: see plan_copies
+  int copy_row, copy_bytes, copy_off;
+  const uint8_t *copy_src;
+  int64_t copy_step;
   volatile int *abort;
   uint32_t limit;
 
@@ -411,7 +415,7 @@ struct BnGroup {
     abort = ab;
     limit = a.wait_limit;
     if (t == 0) {
-      for (int i = 0; i < stages; ++i) tc::mbar_init(bars + 8u * i, 1);
+      for (int i = 0; i < stages; ++i) tc::mbar_init(bars + 8u * i, 4 * R);      // one arrival per copy
       tc::fence_barrier_init();
     }
     if (threadIdx.x == 0) *abort = 0;
@@ -423,17 +427,34 @@ struct BnGroup {
     if (wpr == 1) __syncwarp();
     else asm volatile("bar.sync %0, %1;" ::"r"(1 + sub), "r"(tpr) : "memory");
   }
-  // Thread 0 of the group: copies the next `rows` rows into the next stage; src and
-  // step: row 0 of each tensor and the bytes from a row to the next.
-  __device__ __forceinline__ void fetch(int rows, const uint8_t *const (&src)[4], const int64_t (&step)[4]) {
+  // Which copies of a batch this thread issues: copy c is tensor c % 4 of row c / 4,
+  // warp c % wpr's lane c / wpr has it (issuing takes a thread some 200 cycles; eight
+  // copies by one thread held the others up at the next barrier for 1900 of 9000
+  // cycles).  src: the first row of each tensor, step: bytes from a row to the next.
+  __device__ __forceinline__ void plan_copies(const uint8_t *s0, const uint8_t *s1, const uint8_t *s2, const uint8_t *s3,
+                                              int64_t d0, int64_t d1, int64_t d2, int64_t d3) {
+    const int c = warp + wpr * (threadIdx.x & 31), k = c & 3;
+    issues = c < 4 * R;
+    copy_row = c >> 2;
+    const int64_t d = k == 0 ? d0 : k == 1 ? d1 : k == 2 ? d2 : d3;
+    copy_bytes = k == 0 ? row_bytes[0] : k == 1 ? row_bytes[1] : k == 2 ? row_bytes[2] : row_bytes[3];
+    copy_off = (k == 0 ? off[0] : k == 1 ? off[1] : k == 2 ? off[2] : off[3]) + copy_row * copy_bytes;
+    copy_src = (k == 0 ? s0 : k == 1 ? s1 : k == 2 ? s2 : s3) + copy_row * d;
+    copy_step = R * d;
+  }
+  // The next batch, of `rows` rows, into the next stage; called by the whole group.
+  __device__ __forceinline__ void fetch(int rows) {
     const uint32_t bar = bars + 8u * st_put;
-    tc::mbar_expect_tx(bar, rows * bytes_per_row);
-    const uint32_t dst = ring_addr + st_put * stage_bytes;
-    for (int i = 0; i < rows; ++i) {
-#pragma unroll
-      for (int k = 0; k < 4; ++k)
-        if (row_bytes[k]) tc::bulk_load(dst + off[k] + i * row_bytes[k], src[k] + i * step[k], row_bytes[k], bar);
+    if (issues) {
+      if (copy_row < rows && copy_bytes) {
+        tc::mbar_expect_tx(bar, copy_bytes);
+        tc::bulk_load(ring_addr + st_put * stage_bytes + copy_off, copy_src, copy_bytes, bar);
+      } else {
+        tc::mbar_arrive(bar);
+      }
+      copy_src += copy_step;
     }
+    __syncwarp();
     if (++st_put == stages) st_put = 0;
   }
   // The next stage.  A wait that runs out latches PRISM_ETIMEOUT; the group goes on
@@ -514,8 +535,9 @@ struct BnGroup {
 // Rows per batch: registers hold R rows of values beside the column sums.
 constexpr int bn_bwd_rows(int V) { return V == 1 ? 2 : 1; }
 
-template <typename TX, typename TY, int V>
-__global__ void __launch_bounds__(kBnMaxThreads) block_norm_bwd_kernel(const BlockNormArgs a) {
+// kThreads: the most threads it is launched with (fewer leave it more registers).
+template <typename TX, typename TY, int V, int kThreads>
+__global__ void __launch_bounds__(kThreads) block_norm_bwd_kernel(const BlockNormArgs a) {
   constexpr int R = bn_bwd_rows(V);
   extern __shared__ __align__(16) uint8_t bn_smem[];
   __shared__ uint64_t mbars[kBnMaxGroups * kBnMaxStages];
@@ -536,17 +558,11 @@ __global__ void __launch_bounds__(kBnMaxThreads) block_norm_bwd_kernel(const Blo
   // the group's rows are consecutive
   const int per = (r1 - r0 + a.groups - 1) / a.groups;
   const int first = r0 + g.sub * per, rows = max(0, min(per, r1 - first)), batches = (rows + R - 1) / R;
-  const int64_t step[4] = {a.sxo * (int64_t)sizeof(TX), a.sdh * (int64_t)sizeof(TY), a.sdxo * (int64_t)sizeof(TX),
-                           a.sy * (int64_t)sizeof(TY)};
-  auto fetch = [&](int it) {
-    const int64_t r = first + (int64_t)it * R;
-    const uint8_t *const src[4] = {
-        reinterpret_cast<const uint8_t *>(xo + r * a.sxo), reinterpret_cast<const uint8_t *>(dh + r * a.sdh),
-        reinterpret_cast<const uint8_t *>(dxo + r * a.sdxo), reinterpret_cast<const uint8_t *>(y + r * a.sy)};
-    g.fetch(min(R, rows - it * R), src, step);
-  };
-  if (g.t == 0)
-    for (int it = 0; it < min(batches, a.stages); ++it) fetch(it);
+  g.plan_copies(reinterpret_cast<const uint8_t *>(xo + first * a.sxo), reinterpret_cast<const uint8_t *>(dh + first * a.sdh),
+                reinterpret_cast<const uint8_t *>(dxo + first * a.sdxo), reinterpret_cast<const uint8_t *>(y + first * a.sy),
+                a.sxo * (int64_t)sizeof(TX), a.sdh * (int64_t)sizeof(TY), a.sdxo * (int64_t)sizeof(TX),
+                a.sy * (int64_t)sizeof(TY));
+  for (int it = 0; it < min(batches, a.stages); ++it) g.fetch(min(R, rows - it * R));
   float2 A1[4], G1[4];      // V = 1
 #pragma unroll
   for (int e = 0; e < 4; ++e) A1[e] = G1[e] = both(0.f);
@@ -715,7 +731,7 @@ __global__ void __launch_bounds__(kBnMaxThreads) block_norm_bwd_kernel(const Blo
     }
     if (!py || g.wpr == 1) g.sync();
     // every thread of the group has read the stage: its next rows may land there
-    if (g.t == 0 && it + a.stages < batches) fetch(it + a.stages);
+    if (it + a.stages < batches) g.fetch(min(R, rows - (it + a.stages) * R));
     if (y) {
 #pragma unroll
       for (int i = 0; i < R; ++i)

@@ -326,15 +326,17 @@ static int launch_norm_fwd(const prism_norm_params *p, BlockNormArgs &a, cudaStr
     default: return launch_norm_fwd_v<TX, TY, 8>(s, a, st);
   }
 }
-template <typename TX, typename TY, int V>
+template <typename TX, typename TY, int V, int kThreads>
 static int launch_norm_bwd_v(const NormBwdShape &s, const BlockNormArgs &a, cudaStream_t st) {
-  cudaFuncSetAttribute(block_norm_bwd_kernel<TX, TY, V>, cudaFuncAttributeMaxDynamicSharedMemorySize, kBnSmem);
-  PRISM_TRACED("block_norm_bwd_kernel", st, block_norm_bwd_kernel<TX, TY, V><<<(unsigned)s.slots, s.threads, s.smem, st>>>(a));
+  const auto kernel = block_norm_bwd_kernel<TX, TY, V, kThreads>;
+  cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kBnSmem);
+  PRISM_TRACED("block_norm_bwd_kernel", st, kernel<<<(unsigned)s.slots, s.threads, s.smem, st>>>(a));
   return PRISM_OK;
 }
 template <typename TX, typename TY>
 static int launch_norm_bwd(const NormBwdShape &s, const BlockNormArgs &a, cudaStream_t st) {
-  return s.V == 1 ? launch_norm_bwd_v<TX, TY, 1>(s, a, st) : launch_norm_bwd_v<TX, TY, 2>(s, a, st);
+  return s.V == 1 ? launch_norm_bwd_v<TX, TY, 1, 512>(s, a, st)
+                  : s.threads <= 320 ? launch_norm_bwd_v<TX, TY, 2, 320>(s, a, st) : launch_norm_bwd_v<TX, TY, 2, 512>(s, a, st);
 }
 
 }  // namespace prism
