@@ -48,37 +48,53 @@ struct PackedSeq {
   }
 };
 
-// Per query row and head (half a warp for head_dim 64, a warp for 128): D =
-// rowsum(dO o (O + residual)) and LSE log2e; a row that sees nothing gets +inf,
-// so that its probabilities 2^(x - inf) are zero.  Written in flattened order.
+// Per query row and head (8 or 16 lanes, 8 columns each; two rows at a time, so that
+// six 16-byte loads are in flight): D = rowsum(dO o (O + residual)) and LSE log2e; a
+// row that sees nothing gets +inf, so that its probabilities 2^(x - inf) are zero.
+// Written in flattened order.
 template <int D>
 __global__ void __launch_bounds__(256) packed_stats_kernel(const PackedArgs a, const __nv_bfloat16 *__restrict__ o,
                                                            float *__restrict__ delta, float *__restrict__ lse2) {
-  constexpr int kLanes = D / 4;
-  const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) / kLanes;   // row * heads + head
+  constexpr int kLanes = D / 8, kRows = 256 / kLanes;      // (row, head) pairs of a CTA and pass
   const int sub = threadIdx.x % kLanes;
-  float s = 0.f;
-  const bool in = i < (int64_t)a.qs.rows * a.heads;
-  const int64_t row = i / a.heads;
-  const int h = (int)(i - row * a.heads);
-  if (in) {
-    const uint2 uo = *reinterpret_cast<const uint2 *>(o + row * a.so[0] + h * a.so[1] + sub * 4);
-    const uint2 ug = *reinterpret_cast<const uint2 *>(a.dout + row * a.sdo[0] + h * a.sdo[1] + sub * 4);
-    float o0 = bf16_lo(uo.x), o1 = bf16_hi(uo.x), o2 = bf16_lo(uo.y), o3 = bf16_hi(uo.y);
-    if (a.o_res) {
-      const uint2 ur = *reinterpret_cast<const uint2 *>(a.o_res + i * D + sub * 4);
-      o0 += bf16_lo(ur.x); o1 += bf16_hi(ur.x); o2 += bf16_lo(ur.y); o3 += bf16_hi(ur.y);
+  const int64_t total = (int64_t)a.qs.rows * a.heads;
+  uint4 uo[2], ug[2], ur[2];
+  int64_t row[2];
+  int h[2];
+  float L[2];
+#pragma unroll
+  for (int p = 0; p < 2; ++p) {
+    const int64_t i = (int64_t)blockIdx.x * (2 * kRows) + p * kRows + threadIdx.x / kLanes;   // row * heads + head
+    row[p] = i / a.heads;
+    h[p] = (int)(i - row[p] * a.heads);
+    uo[p] = ug[p] = ur[p] = make_uint4(0u, 0u, 0u, 0u);
+    if (i < total) {
+      uo[p] = __ldg(reinterpret_cast<const uint4 *>(o + row[p] * a.so[0] + h[p] * a.so[1] + sub * 8));
+      ug[p] = __ldg(reinterpret_cast<const uint4 *>(a.dout + row[p] * a.sdo[0] + h[p] * a.sdo[1] + sub * 8));
+      if (a.o_res) ur[p] = __ldg(reinterpret_cast<const uint4 *>(a.o_res + i * D + sub * 8));
+      L[p] = a.lse[(int64_t)h[p] * a.qs.rows + row[p]];
+    } else {
+      row[p] = -1;
     }
-    s = (o0 * bf16_lo(ug.x) + o1 * bf16_hi(ug.x)) + (o2 * bf16_lo(ug.y) + o3 * bf16_hi(ug.y));
   }
 #pragma unroll
-  for (int w = kLanes / 2; w > 0; w >>= 1) s += __shfl_xor_sync(0xffffffffu, s, w);
-  if (in && sub == 0) {
-    const float L = a.lse[(int64_t)h * a.qs.rows + row];
-    const int kvh = h / a.group;
-    const int64_t at = ((int64_t)kvh * a.qs.rows + row) * a.group + h - kvh * a.group;
-    delta[at] = s;
-    lse2[at] = isfinite(L) ? L * kLog2e : INFINITY;
+  for (int p = 0; p < 2; ++p) {
+    const uint32_t wo[4] = {uo[p].x, uo[p].y, uo[p].z, uo[p].w}, wg[4] = {ug[p].x, ug[p].y, ug[p].z, ug[p].w},
+                   wr[4] = {ur[p].x, ur[p].y, ur[p].z, ur[p].w};
+    float s = 0.f;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      s = fmaf(bf16_lo(wo[e]) + bf16_lo(wr[e]), bf16_lo(wg[e]), s);
+      s = fmaf(bf16_hi(wo[e]) + bf16_hi(wr[e]), bf16_hi(wg[e]), s);
+    }
+#pragma unroll
+    for (int w = kLanes / 2; w > 0; w >>= 1) s += __shfl_xor_sync(0xffffffffu, s, w);
+    if (row[p] >= 0 && sub == 0) {
+      const int kvh = h[p] / a.group;
+      const int64_t at = ((int64_t)kvh * a.qs.rows + row[p]) * a.group + h[p] - kvh * a.group;
+      delta[at] = s;
+      lse2[at] = isfinite(L[p]) ? L[p] * kLog2e : INFINITY;
+    }
   }
 }
 

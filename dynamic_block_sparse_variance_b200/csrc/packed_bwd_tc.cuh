@@ -100,10 +100,50 @@ __device__ __forceinline__ void store_row(uint32_t taddr, bool have, bool zero, 
   }
 }
 
+// The same in fp32 to the layout of PackedParts, zeros where not `keep`; out: the
+// row's place for the first of the columns.
+template <int COLS>
+__device__ __forceinline__ void store_part(uint32_t taddr, bool keep, float *out) {
+#pragma unroll
+  for (int c = 0; c < COLS / 32; ++c) {
+    uint32_t v[32];
+    tc::tmem_ld32(taddr + 32u * c, v);
+    tc::tmem_ld_wait();
+#pragma unroll
+    for (int e = 0; e < 32; e += 4)
+      *reinterpret_cast<uint4 *>(out + (8 * c + e / 4) * 512) =
+          keep ? make_uint4(v[e], v[e + 1], v[e + 2], v[e + 3]) : make_uint4(0u, 0u, 0u, 0u);
+  }
+}
+
+// The query tiles (of tt tokens) that see keys from key0 on, and how they are cut.
+// A keys CTA walks 4 products per tile, 2 us, and with grouped heads or few CTAs the
+// longest walk can take longer than all the rest: `splits` CTAs share it, each writes
+// its dK and dV in fp32, and packed_sum_kernel adds them in order.  A share has at
+// least 6 tiles, so short walks stay whole and are written at once.
+struct KeyWalk {
+  int tt, behind, first, steps, chunk, shares;
+  __device__ __forceinline__ KeyWalk(const PackedArgs &a, const PackedSeq &s, int key0, int splits) {
+    tt = 128 / a.group;
+    behind = a.causal ? s.lk - s.lq : 0x40000000;     // token t sees key j iff t >= j - behind
+    const int ntile = (s.lq + tt - 1) / tt;
+    first = key0 < s.lk ? min(ntile, max(0, key0 - behind) / tt) : ntile;
+    steps = ntile - first;
+    chunk = max(6, (steps + splits - 1) / splits);
+    shares = max(1, (steps + chunk - 1) / chunk);
+  }
+};
+struct PackedParts {
+  int splits;
+  int64_t tiles;      // key tiles times kv heads
+  float *dk, *dv;     // [split][tile][D / 4][128 rows][4]: a warp's 32 rows of 4 columns are consecutive
+};
+
 // The kind that keeps dK and dV; `block`: its number among the CTAs of its kind.
 template <int D>
 __device__ __forceinline__ void packed_keys_cta(const CUtensorMap &tmQ, const CUtensorMap &tmK, const CUtensorMap &tmV,
-                                                const CUtensorMap &tmO, const PackedArgs &a, const uint32_t limit, int block) {
+                                                const CUtensorMap &tmO, const PackedArgs &a, const PackedParts &parts,
+                                                const uint32_t limit, int block) {
   using T = Tile<D>;
   extern __shared__ __align__(1024) uint8_t sgen[];
   const uint32_t sbase = smem_u32(sgen);
@@ -132,19 +172,17 @@ __device__ __forceinline__ void packed_keys_cta(const CUtensorMap &tmQ, const CU
   volatile int *abort = reinterpret_cast<volatile int *>(sgen + (sBar - sbase) + 8 * 20 + 4);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int kvh = block % a.kv_heads, slot = block / a.kv_heads;
+  const int share = block % parts.splits, kvh = block / parts.splits % a.kv_heads, slot = block / parts.splits / a.kv_heads;
   int64_t piece;
   const int b = find_sequence(a.ks, slot, 1, 128, piece);
   PackedSeq s;
   if (!s.load(a, b)) return;
   if (piece < 0 || piece * 128 >= s.room) return;
   const int key0 = (int)piece * 128;
-  // query tiles of `tt` tokens; token t sees key j when j <= t + lk - lq (causal)
-  const int tt = 128 / a.group;
-  const int behind = a.causal ? s.lk - s.lq : 0x40000000;   // token t sees key j iff t >= j - behind
-  const int ntile = (s.lq + tt - 1) / tt;
-  const int first = key0 < s.lk ? min(ntile, max(0, key0 - behind) / tt) : ntile;
-  const int nsteps = ntile - first;
+  const KeyWalk walk(a, s, key0, parts.splits);
+  if (share >= walk.shares) return;
+  const int tt = walk.tt, behind = walk.behind;
+  const int first = walk.first + share * walk.chunk, nsteps = min(walk.chunk, walk.steps - share * walk.chunk);
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < 3; ++i) {
@@ -374,21 +412,27 @@ __device__ __forceinline__ void packed_keys_cta(const CUtensorMap &tmQ, const CU
         const int key = key0 + row;
         const bool have = key < s.room;
         const bool zero = nsteps == 0;
-        const float keep = key < s.lk ? 1.f : 0.f;    // rows with room but not in use: zero
+        const bool keep = key < s.lk;                 // rows with room but not in use: zero
         const int64_t r = s.k0 + key;
         constexpr int kCols = D / 2;                  // of each half's warps
         const uint32_t co = lane_off + (uint32_t)(half * kCols);
-        __nv_bfloat16 *dk = a.dk + r * a.sdk[0] + kvh * a.sdk[1] + half * kCols;
-        __nv_bfloat16 *dv = a.dv + r * a.sdv[0] + kvh * a.sdv[1] + half * kCols;
-        if (__any_sync(0xffffffffu, have && keep == 0.f && !zero)) {
-          // a tile with rows behind the keys in use: those rows are zeros, whatever their accumulators hold
-          store_row<kCols>(tdK + co, have && keep != 0.f, zero, a.scale, dk);
-          store_row<kCols>(tdV + co, have && keep != 0.f, zero, 1.f, dv);
-          store_row<kCols>(tdK + co, have && keep == 0.f, true, 0.f, dk);
-          store_row<kCols>(tdV + co, have && keep == 0.f, true, 0.f, dv);
+        if (walk.shares > 1) {
+          const int64_t at = (((int64_t)share * parts.tiles + slot * a.kv_heads + kvh) * (D / 4) + half * (kCols / 4)) * 512 + row * 4;
+          store_part<kCols>(tdK + co, keep, parts.dk + at);
+          store_part<kCols>(tdV + co, keep, parts.dv + at);
         } else {
-          store_row<kCols>(tdK + co, have, zero, a.scale, dk);
-          store_row<kCols>(tdV + co, have, zero, 1.f, dv);
+          __nv_bfloat16 *dk = a.dk + r * a.sdk[0] + kvh * a.sdk[1] + half * kCols;
+          __nv_bfloat16 *dv = a.dv + r * a.sdv[0] + kvh * a.sdv[1] + half * kCols;
+          if (__any_sync(0xffffffffu, have && !keep && !zero)) {
+            // a tile with rows behind the keys in use: those rows are zeros, whatever their accumulators hold
+            store_row<kCols>(tdK + co, have && keep, zero, a.scale, dk);
+            store_row<kCols>(tdV + co, have && keep, zero, 1.f, dv);
+            store_row<kCols>(tdK + co, have && !keep, true, 0.f, dk);
+            store_row<kCols>(tdV + co, have && !keep, true, 0.f, dv);
+          } else {
+            store_row<kCols>(tdK + co, have, zero, a.scale, dk);
+            store_row<kCols>(tdV + co, have, zero, 1.f, dv);
+          }
         }
       }
     }
@@ -652,10 +696,47 @@ template <int D>
 __global__ void __launch_bounds__(kPbThreads, 1)
     packed_bwd_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                          const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmO,
-                         const PackedArgs a, const uint32_t limit, const int key_blocks) {
+                         const PackedArgs a, const PackedParts parts, const uint32_t limit, const int key_blocks) {
   const int block = (int)blockIdx.x;
-  if (block < key_blocks) packed_keys_cta<D>(tmQ, tmK, tmV, tmO, a, limit, block);
+  if (block < key_blocks) packed_keys_cta<D>(tmQ, tmK, tmV, tmO, a, parts, limit, block);
   else packed_queries_cta<D>(tmK, tmV, a, limit, block - key_blocks, (int)gridDim.x - key_blocks);
+}
+
+// Adds the shares of walks that were cut (see KeyWalk), in order: one CTA per (128
+// keys, kv head, 32 columns).
+template <int D>
+__global__ void __launch_bounds__(256) packed_sum_kernel(const PackedArgs a, const PackedParts parts) {
+  const int kvh = (int)(blockIdx.x % a.kv_heads), slot = (int)(blockIdx.x / a.kv_heads);
+  int64_t piece;
+  const int b = find_sequence(a.ks, slot, 1, 128, piece);
+  PackedSeq s;
+  if (!s.load(a, b)) return;
+  if (piece < 0 || piece * 128 >= s.room) return;
+  const int key0 = (int)piece * 128;
+  const KeyWalk walk(a, s, key0, parts.splits);
+  if (walk.shares == 1) return;
+  const int row = threadIdx.x & 127, rows = min(128, s.room - key0);
+  const int64_t step = parts.tiles * (D * 128);
+  const float *const base = (threadIdx.x < 128 ? parts.dk : parts.dv) + ((int64_t)blockIdx.x * (D / 4) + blockIdx.y * 8) * 512 + row * 4;
+  float4 x[8];
+#pragma unroll
+  for (int c = 0; c < 8; ++c) x[c] = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int n = 0; n < walk.shares; ++n) {
+#pragma unroll
+    for (int c = 0; c < 8; ++c) {
+      const float4 p = *reinterpret_cast<const float4 *>(base + n * step + c * 512);
+      x[c].x += p.x; x[c].y += p.y; x[c].z += p.z; x[c].w += p.w;
+    }
+  }
+  if (row >= rows) return;
+  const int64_t r = s.k0 + key0 + row;
+  const float mul = threadIdx.x < 128 ? a.scale : 1.f;
+  __nv_bfloat16 *const out = (threadIdx.x < 128 ? a.dk + r * a.sdk[0] + kvh * a.sdk[1] : a.dv + r * a.sdv[0] + kvh * a.sdv[1]) + blockIdx.y * 32;
+#pragma unroll
+  for (int c = 0; c < 8; c += 2)
+    *reinterpret_cast<uint4 *>(out + 4 * c) =
+        make_uint4(pack_bf16(x[c].x * mul, x[c].y * mul), pack_bf16(x[c].z * mul, x[c].w * mul),
+                   pack_bf16(x[c + 1].x * mul, x[c + 1].y * mul), pack_bf16(x[c + 1].z * mul, x[c + 1].w * mul));
 }
 
 }  // namespace prism

@@ -72,13 +72,27 @@ static int packed_args(const prism_packed_params *p, const void *q, const void *
   return PRISM_OK;
 }
 
+// The backward's cut of long walks over the queries (see KeyWalk): the longest walk
+// is brought down to an even share of all products on 148 SMs, the walks of several
+// sequences, whose lengths the host does not know, to twice that with the longest
+// sequence taken as three times the average.
 struct PackedBwdWs {
-  size_t delta, lse2, total;
+  int splits;
+  int64_t tiles;
+  size_t delta, lse2, dk, dv, total;
   explicit PackedBwdWs(const prism_packed_params *p) {
     const size_t n = (size_t)p->q_rows * p->heads;
+    const double seqs = p->seqs, qt = (double)p->q_rows / seqs * (p->heads / p->kv_heads) / 128, kt = (double)p->k_rows / seqs / 128;
+    const double share = 7.0 * seqs * p->kv_heads * std::max(qt, 1.0) * std::max(kt, 1.0) * (p->causal ? 0.5 : 1.0) / 148;
+    const double longest = 4.0 * qt * (p->seqs > 1 ? 1.5 : 1.0);
+    splits = (int)std::max(1.0, std::min({8.0, std::floor(longest / share), std::floor(longest / 4 / 6)}));
+    tiles = slot_bound(p->k_rows, p->seqs, 1, 128) * p->kv_heads;
     delta = 0;
     lse2 = align256(n * 4);
-    total = lse2 + align256(n * 4);
+    dk = lse2 + align256(n * 4);
+    const size_t part = splits > 1 ? align256((size_t)tiles * splits * 128 * p->head_dim * 4) : 0;
+    dv = dk + part;
+    total = dv + part;
   }
 };
 
@@ -165,8 +179,8 @@ static int launch_packed_fwd(const prism_packed_params *p, const PackedArgs &a, 
 }
 
 template <int D>
-static int launch_packed_bwd(const prism_packed_params *p, const PackedArgs &a, float *delta, float *lse2,
-                             cudaStream_t st) {
+static int launch_packed_bwd(const prism_packed_params *p, const PackedArgs &a, const PackedParts &parts, float *delta,
+                             float *lse2, cudaStream_t st) {
   const int64_t dummy[2] = {D, D};
   const bool keys = p->k_rows > 0, rows = p->q_rows > 0;
   const int tt = 128 / a.group;     // tokens per streamed query tile
@@ -178,15 +192,17 @@ static int launch_packed_bwd(const prism_packed_params *p, const PackedArgs &a, 
       !make_head_map(&to, rows ? (const void *)a.dout : any, D, rows ? a.heads : 1, rows ? p->q_rows : 1, rows ? a.sdo : dummy, a.group, tt))
     return fail(PRISM_ECUDA, "cuTensorMapEncodeTiled failed");
   if (rows) {
-    const int64_t threads = p->q_rows * p->heads * (D / 4);
-    PRISM_TRACED("packed_stats_kernel", st, packed_stats_kernel<D><<<(unsigned)((threads + 255) / 256), 256, 0, st>>>(a, a.o, delta, lse2));
+    const int64_t threads = p->q_rows * p->heads * (D / 8);
+    PRISM_TRACED("packed_stats_kernel", st, packed_stats_kernel<D><<<(unsigned)((threads + 511) / 512), 256, 0, st>>>(a, a.o, delta, lse2));
   }
-  const int64_t key_blocks = keys ? slot_bound(p->k_rows, p->seqs, 1, 128) * a.kv_heads : 0;
+  const int64_t key_tiles = keys ? parts.tiles : 0, key_blocks = key_tiles * parts.splits;
   const int64_t blocks = key_blocks + (rows ? slot_bound(p->q_rows, p->seqs, a.group, 128) * a.kv_heads : 0);
   if (blocks > 0x7fffffffLL) return fail(PRISM_EINVAL, "packed: too many rows");
   if (blocks == 0) return PRISM_OK;
   cudaFuncSetAttribute(packed_bwd_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, kPbSmem<D>);
-  PRISM_TRACED("packed_bwd_tc_kernel", st, packed_bwd_tc_kernel<D><<<(unsigned)blocks, kPbThreads, kPbSmem<D>, st>>>(tq, tk, tv, to, a, wait_limit(), (int)key_blocks));
+  PRISM_TRACED("packed_bwd_tc_kernel", st, packed_bwd_tc_kernel<D><<<(unsigned)blocks, kPbThreads, kPbSmem<D>, st>>>(tq, tk, tv, to, a, parts, wait_limit(), (int)key_blocks));
+  if (parts.splits > 1 && keys)
+    PRISM_TRACED("packed_sum_kernel", st, packed_sum_kernel<D><<<dim3((unsigned)key_tiles, D / 32), 256, 0, st>>>(a, parts));
   return PRISM_OK;
 }
 
@@ -410,7 +426,9 @@ int prism_packed_attn_bwd(const prism_packed_params *p, const void *q, const voi
   a.dk = static_cast<__nv_bfloat16 *>(dk);
   a.dv = static_cast<__nv_bfloat16 *>(dv);
   cudaStream_t st = as_stream(stream);
-  return p->head_dim == 128 ? launch_packed_bwd<128>(p, a, delta, lse2, st) : launch_packed_bwd<64>(p, a, delta, lse2, st);
+  const PackedParts parts{w.splits, w.tiles, reinterpret_cast<float *>(ws + w.dk), reinterpret_cast<float *>(ws + w.dv)};
+  return p->head_dim == 128 ? launch_packed_bwd<128>(p, a, parts, delta, lse2, st)
+                            : launch_packed_bwd<64>(p, a, parts, delta, lse2, st);
 }
 
 int prism_block_norm_fwd(const prism_norm_params *p, const void *x, const void *y, const int32_t *off,
