@@ -15,6 +15,7 @@ struct PackedArgs {
   Offsets qs, ks;
   const int32_t *k_used;
   int heads, kv_heads, group, causal;
+  int debug_stall;                  // test knob (PRISM_OPT_DEBUG_STALL): the first P or dS is never signalled
   float scale, scale_log2;
   const __nv_bfloat16 *q, *k, *v, *dout;
   __nv_bfloat16 *o, *o_res, *dq, *dk, *dv;

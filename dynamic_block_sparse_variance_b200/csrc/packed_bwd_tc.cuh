@@ -394,7 +394,7 @@ __device__ __forceinline__ void packed_keys_cta(const CUtensorMap &tmQ, const CU
       }
       tc::tmem_st_wait();
       tc::tc_fence_before();
-      warp_arrive(b_p);
+      if (!(a.debug_stall && n == 0)) warp_arrive(b_p);
       if (!warp_wait(b_dp, (uint32_t)n & 1u, abort, limit)) {
         ok = false;
         break;
@@ -669,7 +669,7 @@ __device__ __forceinline__ void packed_queries_cta(const CUtensorMap &tmK, const
       form_ds(tDP + lane_off + 64u * half, colS, p, [&](int) { return d4; });
       tc::tmem_st_wait();
       tc::tc_fence_before();
-      warp_arrive(b_ds);
+      if (!(a.debug_stall && n == 0)) warp_arrive(b_ds);
     }
     if (__all_sync(0xffffffffu, ok && !*abort)) {
       if (nsteps > 0) ok = warp_wait(b_drain, 0, abort, limit);

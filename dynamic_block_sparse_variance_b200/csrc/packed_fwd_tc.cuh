@@ -373,7 +373,7 @@ __global__ void __launch_bounds__(64 + 128 * NG, 3 - NG)
       l_run += ((r2[0].x + r2[0].y) + (r2[1].x + r2[1].y)) + ((r2[2].x + r2[2].y) + (r2[3].x + r2[3].y));
       tc::tmem_st_wait();
       tc::tc_fence_before();
-      warp_arrive(b_pfull(g));
+      if (!(a.debug_stall && n == 0)) warp_arrive(b_pfull(g));
     }
     // epilogue
     if (__all_sync(0xffffffffu, ok && !*abort)) {

@@ -64,6 +64,7 @@ static int packed_args(const prism_packed_params *p, const void *q, const void *
   a->kv_heads = p->kv_heads;
   a->group = p->heads / p->kv_heads;
   a->causal = p->causal != 0;
+  a->debug_stall = g_debug_stall;
   a->scale = p->scale > 0.f ? p->scale : 1.f / std::sqrt((float)p->head_dim);
   a->scale_log2 = a->scale * kLog2e;
   a->q = static_cast<const __nv_bfloat16 *>(q);

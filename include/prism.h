@@ -463,7 +463,9 @@ int prism_block_norm_bwd(const prism_norm_params *p, const void *x_out, const vo
  *   PRISM_OPT_DEBUG_STALL   test hook: when 1 the forward kernel never signals
  *                           its first probability tile (nor the tensor-core
  *                           backward its first P^T tile), so a bounded wait
- *                           must time out (PRISM_ETIMEOUT), with no trap or hang.
+ *                           must time out (PRISM_ETIMEOUT), with no trap or hang;
+ *                           likewise the tensor-core kernels of the packed
+ *                           attention, forward and backward.
  * Returns PRISM_EINVAL for an unknown option. */
 #define PRISM_OPT_ATTN_BACKEND 0
 #define PRISM_OPT_WAIT_LIMIT 1
