@@ -76,6 +76,50 @@ struct Tile {
   }
 };
 
+// Loads `rows` flattened query rows of a kv head (rows from r0 of a sequence whose first
+// row is q0) into a tile, zeros behind them; `threads` threads, this one being `t`.
+// A thread keeps one 16-byte piece of every (threads / (D / 8))-th row and steps from
+// row to row by additions: row r is token r / group, head r % group.
+template <int D>
+__device__ __forceinline__ void load_rows_async(uint32_t tile, const __nv_bfloat16 *x, const int64_t (&stride)[2], int q0,
+                                                int head0, int group, int r0, int rows, int tile_rows, int t, int threads) {
+  constexpr int CH = D / 8;
+  const int step = threads / CH, dt = step / group, dg = step - dt * group;
+  const int ch = t % CH;
+  int r = t / CH, tok = (r0 + r) / group, g = r0 + r - tok * group;
+  const __nv_bfloat16 *const base = x + (int64_t)q0 * stride[0] + (int64_t)head0 * stride[1] + ch * 8;
+  for (; r < tile_rows; r += step) {
+    const bool have = r < rows;
+    cp_async16_or_zero(tile + (uint32_t)(r >> 7) * Tile<D>::kBytes + Tile<D>::off(r & 127, ch),
+                       have ? base + tok * stride[0] + g * stride[1] : base, have);
+    tok += dt;
+    g += dg;
+    if (g >= group) {
+      g -= group;
+      ++tok;
+    }
+  }
+}
+
+// A warp's 32 rows of D bf16, which it has put into rows [row0, row0 + 32) of a tile in
+// shared memory, to their places in global memory, whole rows at a time (straight
+// from the registers, a row per lane, every store would touch 32 rows).  dst: this
+// lane's row, nullptr for none.
+template <int D>
+__device__ __forceinline__ void flush_rows(const uint8_t *tile, int row0, __nv_bfloat16 *dst) {
+  constexpr int CH = D / 8;
+  const int lane = threadIdx.x & 31, ch = lane % CH;
+  __syncwarp();
+#pragma unroll 4
+  for (int i = 0; i < CH; ++i) {      // 32 / CH rows at a time
+    const int r = i * (32 / CH) + lane / CH;
+    __nv_bfloat16 *const p = reinterpret_cast<__nv_bfloat16 *>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(dst), r));
+    const uint4 w = *reinterpret_cast<const uint4 *>(tile + Tile<D>::off(row0 + r, ch));
+    if (p) *reinterpret_cast<uint4 *>(p + ch * 8) = w;
+  }
+  __syncwarp();
+}
+
 struct PackedSplit {
   int splits;
   float *o;     // [split][q_rows][heads][D]
@@ -97,7 +141,7 @@ __global__ void __launch_bounds__(64 + 128 * NG, 3 - NG)
     packed_fwd_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                          const PackedArgs a, const PackedSplit sp, const uint32_t limit) {
   using T = Tile<D>;
-  constexpr int kStages = PfCfg<D, NG>::kStages, kThreads = PfCfg<D, NG>::kThreads;
+  constexpr int kStages = PfCfg<D, NG>::kStages;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t sbase = (smem_u32(smem_raw) + 1023u) & ~1023u;
   uint8_t *sgen = smem_raw + (sbase - smem_u32(smem_raw));
@@ -113,6 +157,7 @@ __global__ void __launch_bounds__(64 + 128 * NG, 3 - NG)
   auto b_pfull = [&](int g) { return sBar + 8u * (18 + g); };
   const uint32_t b_edge = sBar + 8u * 20;    // the edge tile of V landed
   const uint32_t b_drain = sBar + 8u * 21;
+  const uint32_t b_q = sBar + 8u * 22;       // Q is in shared memory (an arrival per softmax warp)
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sgen + (sBar - sbase) + 8 * 24);
   volatile int *abort = reinterpret_cast<volatile int *>(sgen + (sBar - sbase) + 8 * 24 + 4);
 
@@ -159,6 +204,7 @@ __global__ void __launch_bounds__(64 + 128 * NG, 3 - NG)
     }
     tc::mbar_init(b_edge, 1);
     tc::mbar_init(b_drain, 1);
+    tc::mbar_init(b_q, 4 * NG);
     *abort = 0;
     tc::fence_barrier_init();
   }
@@ -166,17 +212,6 @@ __global__ void __launch_bounds__(64 + 128 * NG, 3 - NG)
     tc::tmem_alloc(smem_u32(tmem_slot), 256 * NG);
     tc::tmem_relinquish();
   }
-  // Q: flattened row r0 + r is token (r0 + r) / group, head kvh group + (r0 + r) % group
-  for (int i = threadIdx.x; i < 128 * NG * (D / 8); i += kThreads) {
-    const int r = i / (D / 8), ch = i % (D / 8);
-    const bool have = r < rows;
-    const int fr = r0 + (have ? r : 0), tok = fr / a.group;
-    const __nv_bfloat16 *src = a.q + (int64_t)(s.q0 + tok) * a.sq[0] + (int64_t)(kvh * a.group + fr - tok * a.group) * a.sq[1] + ch * 8;
-    cp_async16_or_zero(sQ(r >> 7) + T::off(r & 127, ch), src, have);
-  }
-  cp_async_commit();
-  cp_async_wait<0>();
-  fence_async_smem();
   tc::tc_fence_before();
   __syncthreads();
   tc::tc_fence_after();
@@ -260,7 +295,7 @@ __global__ void __launch_bounds__(64 + 128 * NG, 3 - NG)
       };
       // S of step 0, then per step PV_A S_A(+1) PV_B S_B(+1): one tile's softmax
       // runs while the other tile's products execute
-      bool ok = n_all == 0 || wait_full(b_kfull(0), 0);
+      bool ok = n_all == 0 || (tc::mbar_wait(b_q, 0, abort, limit) && wait_full(b_kfull(0), 0));
       if (ok && n_all > 0) {
         for (int g = 0; g < NG; ++g)
           if (n_g[g] > 0) issue_s(0, g);
@@ -300,6 +335,13 @@ __global__ void __launch_bounds__(64 + 128 * NG, 3 - NG)
     const int fr = r0 + row, tok = have ? fr / a.group : 0;
     const int vis = have ? s.visible(a, tok) : 0;
     const float sl2 = a.scale_log2;
+    // Q while the first tiles of K and V are on their way
+    if (t0 < tend)
+      load_rows_async<D>(sQ(0), a.q, a.sq, s.q0, kvh * a.group, a.group, r0, rows, 128 * NG, (int)threadIdx.x - 64, 128 * NG);
+    cp_async_commit();
+    cp_async_wait<0>();
+    fence_async_smem();
+    warp_arrive(b_q);
     float m_run = -INFINITY, l_run = 0.f;
     bool ok = true;
     const int steps = t1[g] - t0;
@@ -385,46 +427,59 @@ __global__ void __launch_bounds__(64 + 128 * NG, 3 - NG)
         const float inv = l_run > 0.f ? 1.f / l_run : 0.f;
         const int head = kvh * a.group + fr - tok * a.group;
         const int64_t grow_ = s.q0 + tok;
-        __nv_bfloat16 *orow = a.o + grow_ * a.so[0] + head * a.so[1];
-        __nv_bfloat16 *rrow = a.o_res ? a.o_res + (grow_ * a.heads + head) * D : nullptr;
-        float *prow = sp.splits > 1 ? sp.o + (((int64_t)blockIdx.z * a.qs.rows + grow_) * a.heads + head) * D : nullptr;
-#pragma unroll
-        for (int c = 0; c < D / 32; ++c) {
-          uint32_t ov[32];
+        const auto load_o = [&](int c, uint32_t (&v)[32]) {
           if (steps > 0) {
-            tc::tmem_ld32(tO(g) + lane_off + 32u * c, ov);
+            tc::tmem_ld32(tO(g) + lane_off + 32u * c, v);
             tc::tmem_ld_wait();
           } else {
 #pragma unroll
-            for (int e = 0; e < 32; ++e) ov[e] = 0u;
+            for (int e = 0; e < 32; ++e) v[e] = 0u;
           }
-          if (have && prow) {
+        };
+        if (sp.splits > 1) {
+          float *const prow = sp.o + (((int64_t)blockIdx.z * a.qs.rows + grow_) * a.heads + head) * D;
 #pragma unroll
-            for (int e = 0; e < 32; e += 4)
-              *reinterpret_cast<float4 *>(prow + 32 * c + e) =
-                  make_float4(__uint_as_float(ov[e]) * inv, __uint_as_float(ov[e + 1]) * inv,
-                              __uint_as_float(ov[e + 2]) * inv, __uint_as_float(ov[e + 3]) * inv);
-          } else if (have) {
+          for (int c = 0; c < D / 32; ++c) {
+            uint32_t ov[32];
+            load_o(c, ov);
+            if (have) {
 #pragma unroll
-            for (int v8 = 0; v8 < 4; ++v8) {
-              uint4 u, r;
-              uint32_t *up = &u.x, *rp = &r.x;
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const float x0 = __uint_as_float(ov[8 * v8 + 2 * e]) * inv;
-                const float x1 = __uint_as_float(ov[8 * v8 + 2 * e + 1]) * inv;
-                up[e] = pack_bf16(x0, x1);
-                rp[e] = pack_bf16(x0 - bf16_lo(up[e]), x1 - bf16_hi(up[e]));
-              }
-              *reinterpret_cast<uint4 *>(orow + 32 * c + 8 * v8) = u;
-              if (rrow) *reinterpret_cast<uint4 *>(rrow + 32 * c + 8 * v8) = r;
+              for (int e = 0; e < 32; e += 4)
+                *reinterpret_cast<float4 *>(prow + 32 * c + e) =
+                    make_float4(__uint_as_float(ov[e]) * inv, __uint_as_float(ov[e + 1]) * inv,
+                                __uint_as_float(ov[e + 2]) * inv, __uint_as_float(ov[e + 3]) * inv);
             }
+            __syncwarp();
           }
-          __syncwarp();   // the next tensor-memory load is warp-collective
+        } else {
+          // every product that reads this tile of Q is done: its memory takes the rows of
+          // O, then those of its rounding residual
+          uint8_t *const tile = sgen + (sQ(g) - sbase);
+          for (int pass = 0; pass < (a.o_res ? 2 : 1); ++pass) {
+#pragma unroll
+            for (int c = 0; c < D / 32; ++c) {
+              uint32_t ov[32];
+              load_o(c, ov);
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                uint4 w;
+                uint32_t *const wp = &w.x;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  const float x0 = __uint_as_float(ov[8 * j + 2 * e]) * inv, x1 = __uint_as_float(ov[8 * j + 2 * e + 1]) * inv;
+                  const uint32_t u = pack_bf16(x0, x1);
+                  wp[e] = pass ? pack_bf16(x0 - bf16_lo(u), x1 - bf16_hi(u)) : u;
+                }
+                *reinterpret_cast<uint4 *>(tile + T::off(32 * q + lane, 4 * c + j)) = w;
+              }
+            }
+            __nv_bfloat16 *const dst = pass ? a.o_res + (grow_ * a.heads + head) * D : a.o + grow_ * a.so[0] + head * a.so[1];
+            flush_rows<D>(tile, 32 * q, have ? dst : nullptr);
+          }
         }
         if (have) {
           const float l2 = l_run > 0.f ? m_run + log2f(l_run) : -INFINITY;
-          if (prow) sp.lse2[((int64_t)blockIdx.z * a.heads + head) * a.qs.rows + grow_] = l2;
+          if (sp.splits > 1) sp.lse2[((int64_t)blockIdx.z * a.heads + head) * a.qs.rows + grow_] = l2;
           else a.lse[(int64_t)head * a.qs.rows + grow_] = l2 * kLn2;
         }
       }
