@@ -7,9 +7,9 @@
 // Warps: 0 TMA producer, 1 MMA issuer and tensor-memory owner, 2-5 and 6-9
 // softmax of tile A and B, one thread per row (its tensor-memory lane).
 //
-// Q comes in through cp.async, because a tile's flattened rows are runs of
-// heads whose length need not divide 128; K and V through TMA tiles of a 3-D
-// map (head_dim, kv head, row).  A key tile that reaches past its sequence's
+// K and V come in through TMA tiles of a 3-D map (head_dim, head, row), Q likewise
+// where the group's size divides 128 (boxes of 128 / group tokens of the group's
+// heads), otherwise through cp.async, row by row.  A key tile that reaches past its sequence's
 // keys holds other rows: their scores are replaced by -inf before they are
 // used, and their values by zeros in shared memory (0 x NaN would not be 0).
 //
@@ -138,7 +138,7 @@ struct PfCfg {
 
 template <int D, int NG>
 __global__ void __launch_bounds__(64 + 128 * NG, 3 - NG)
-    packed_fwd_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+    packed_fwd_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                          const PackedArgs a, const PackedSplit sp, const uint32_t limit) {
   using T = Tile<D>;
   constexpr int kStages = PfCfg<D, NG>::kStages;
@@ -157,7 +157,7 @@ __global__ void __launch_bounds__(64 + 128 * NG, 3 - NG)
   auto b_pfull = [&](int g) { return sBar + 8u * (18 + g); };
   const uint32_t b_edge = sBar + 8u * 20;    // the edge tile of V landed
   const uint32_t b_drain = sBar + 8u * 21;
-  const uint32_t b_q = sBar + 8u * 22;       // Q is in shared memory (an arrival per softmax warp)
+  const uint32_t b_q = sBar + 8u * 22;       // Q is in shared memory (the copy, or an arrival per softmax warp)
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sgen + (sBar - sbase) + 8 * 24);
   volatile int *abort = reinterpret_cast<volatile int *>(sgen + (sBar - sbase) + 8 * 24 + 4);
 
@@ -190,6 +190,7 @@ __global__ void __launch_bounds__(64 + 128 * NG, 3 - NG)
     for (int g = 0; g < NG; ++g) t1[g] = max(t0, min(te, top[g]));
   }
   const int tend = max(t1[0], t1[NG - 1]);
+  const bool q_copy = 128 % a.group == 0;
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < kStages; ++i) {
@@ -204,7 +205,7 @@ __global__ void __launch_bounds__(64 + 128 * NG, 3 - NG)
     }
     tc::mbar_init(b_edge, 1);
     tc::mbar_init(b_drain, 1);
-    tc::mbar_init(b_q, 4 * NG);
+    tc::mbar_init(b_q, q_copy ? 1 : 4 * NG);
     *abort = 0;
     tc::fence_barrier_init();
   }
@@ -224,6 +225,16 @@ __global__ void __launch_bounds__(64 + 128 * NG, 3 - NG)
     if (lane == 0) {
       tc::prefetch_tmap(&tmK);
       tc::prefetch_tmap(&tmV);
+    }
+    if (lane == 0 && q_copy && t0 < tend) {
+      // rows behind the sequence's last one are whatever lies there: no other row's
+      // result depends on them, and theirs are not stored
+      tc::mbar_expect_tx(b_q, NG * T::kBytes);
+#pragma unroll
+      for (int g = 0; g < NG; ++g)
+#pragma unroll
+        for (int c = 0; c < T::kAtoms; ++c)
+          tma_load_3d(sQ(g) + c * T::kAtom, &tmQ, 64 * c, kvh * a.group, s.q0 + (r0 + 128 * g) / a.group, b_q);
     }
     int nk = 0, nv = 0, edge = 0;
     bool ok = true;
@@ -265,6 +276,7 @@ __global__ void __launch_bounds__(64 + 128 * NG, 3 - NG)
       for (int k = max(0, nv - kStages + edge); k < nv; ++k)
         tc::mbar_wait(b_vfull(k % kStages), (uint32_t)(k / kStages) & 1u, &no_abort, limit);
       if (edge) tc::mbar_wait(b_edge, 0, &no_abort, limit);
+      if (q_copy && t0 < tend) tc::mbar_wait(b_q, 0, &no_abort, limit);
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
@@ -336,12 +348,14 @@ __global__ void __launch_bounds__(64 + 128 * NG, 3 - NG)
     const int vis = have ? s.visible(a, tok) : 0;
     const float sl2 = a.scale_log2;
     // Q while the first tiles of K and V are on their way
-    if (t0 < tend)
+    if (t0 < tend && !q_copy)
       load_rows_async<D>(sQ(0), a.q, a.sq, s.q0, kvh * a.group, a.group, r0, rows, 128 * NG, (int)threadIdx.x - 64, 128 * NG);
-    cp_async_commit();
-    cp_async_wait<0>();
-    fence_async_smem();
-    warp_arrive(b_q);
+    if (!q_copy) {
+      cp_async_commit();
+      cp_async_wait<0>();
+      fence_async_smem();
+      warp_arrive(b_q);
+    }
     float m_run = -INFINITY, l_run = 0.f;
     bool ok = true;
     const int steps = t1[g] - t0;

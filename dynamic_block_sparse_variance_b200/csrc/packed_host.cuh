@@ -148,19 +148,21 @@ static int launch_packed_fwd_rows(const prism_packed_params *p, const PackedArgs
 
 template <int D, int NG>
 static int launch_packed_fwd_tc(const prism_packed_params *p, const PackedArgs &a, const PackedSplit &sp, cudaStream_t st) {
-  CUtensorMap tk, tv;
+  CUtensorMap tq, tk, tv;
   // without keys nothing is loaded: the maps then only need to be well formed
   const bool keys = p->k_rows > 0;
   const int64_t dummy[2] = {D, D};
   if (!make_head_map(&tk, keys ? (const void *)a.k : a.q, D, keys ? a.kv_heads : 1, keys ? p->k_rows : 1, keys ? a.sk : dummy) ||
       !make_head_map(&tv, keys ? (const void *)a.v : a.q, D, keys ? a.kv_heads : 1, keys ? p->k_rows : 1, keys ? a.sv : dummy))
     return fail(PRISM_ECUDA, "cuTensorMapEncodeTiled failed");
+  if (!make_head_map(&tq, a.q, D, a.heads, p->q_rows, a.sq, 128 % a.group ? 1 : a.group, 128 % a.group ? 128 : 128 / a.group))
+    return fail(PRISM_ECUDA, "cuTensorMapEncodeTiled failed");
   using Cfg = PfCfg<D, NG>;
   cudaFuncSetAttribute(packed_fwd_tc_kernel<D, NG>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::kSmem);
   const int64_t slots = slot_bound(p->q_rows, p->seqs, a.group, 128 * NG);
   if (slots * a.kv_heads > 0x7fffffffLL) return fail(PRISM_EINVAL, "packed: too many query rows");
   const dim3 grid((unsigned)(slots * a.kv_heads), 1, sp.splits);
-  PRISM_TRACED("packed_fwd_tc_kernel", st, packed_fwd_tc_kernel<D, NG><<<grid, Cfg::kThreads, Cfg::kSmem, st>>>(tk, tv, a, sp, wait_limit()));
+  PRISM_TRACED("packed_fwd_tc_kernel", st, packed_fwd_tc_kernel<D, NG><<<grid, Cfg::kThreads, Cfg::kSmem, st>>>(tq, tk, tv, a, sp, wait_limit()));
   return PRISM_OK;
 }
 
