@@ -72,35 +72,28 @@ __device__ __forceinline__ void form_ds(uint32_t src, uint32_t dst, const uint32
   }
 }
 
-// One 64-column half of an accumulator row, times `mul`, as bf16.
-template <int COLS>
-__device__ __forceinline__ void store_row(uint32_t taddr, bool have, bool zero, float mul, __nv_bfloat16 *out) {
+// COLS columns of an accumulator row (zeros where `zero`), times `mul`, as bf16 into row
+// `row` of a tile in shared memory, from piece ch0 on.
+template <int D, int COLS>
+__device__ __forceinline__ void put_row(uint32_t taddr, bool zero, float mul, uint8_t *tile, int row, int ch0) {
 #pragma unroll
   for (int c = 0; c < COLS / 32; ++c) {
     uint32_t v[32];
-    if (zero) {
+    tc::tmem_ld32(taddr + 32u * c, v);
+    tc::tmem_ld_wait();
 #pragma unroll
-      for (int e = 0; e < 32; ++e) v[e] = 0u;
-    } else {
-      tc::tmem_ld32(taddr + 32u * c, v);
-      tc::tmem_ld_wait();
+    for (int j = 0; j < 4; ++j) {
+      uint4 w;
+      uint32_t *const wp = &w.x;
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        wp[e] = zero ? 0u : pack_bf16(__uint_as_float(v[8 * j + 2 * e]) * mul, __uint_as_float(v[8 * j + 2 * e + 1]) * mul);
+      *reinterpret_cast<uint4 *>(tile + Tile<D>::off(row, ch0 + 4 * c + j)) = w;
     }
-    if (have) {
-#pragma unroll
-      for (int v8 = 0; v8 < 4; ++v8) {
-        uint4 w;
-        uint32_t *wp = &w.x;
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          wp[e] = pack_bf16(__uint_as_float(v[8 * v8 + 2 * e]) * mul, __uint_as_float(v[8 * v8 + 2 * e + 1]) * mul);
-        *reinterpret_cast<uint4 *>(out + 32 * c + 8 * v8) = w;
-      }
-    }
-    __syncwarp();
   }
 }
 
-// The same in fp32 to the layout of PackedParts, zeros where not `keep`; out: the
+// COLS columns of an accumulator row in fp32 to the layout of PackedParts, zeros where not `keep`; out: the
 // row's place for the first of the columns.
 template <int COLS>
 __device__ __forceinline__ void store_part(uint32_t taddr, bool keep, float *out) {
@@ -421,18 +414,14 @@ __device__ __forceinline__ void packed_keys_cta(const CUtensorMap &tmQ, const CU
           store_part<kCols>(tdK + co, keep, parts.dk + at);
           store_part<kCols>(tdV + co, keep, parts.dv + at);
         } else {
-          __nv_bfloat16 *dk = a.dk + r * a.sdk[0] + kvh * a.sdk[1] + half * kCols;
-          __nv_bfloat16 *dv = a.dv + r * a.sdv[0] + kvh * a.sdv[1] + half * kCols;
-          if (__any_sync(0xffffffffu, have && !keep && !zero)) {
-            // a tile with rows behind the keys in use: those rows are zeros, whatever their accumulators hold
-            store_row<kCols>(tdK + co, have && keep, zero, a.scale, dk);
-            store_row<kCols>(tdV + co, have && keep, zero, 1.f, dv);
-            store_row<kCols>(tdK + co, have && !keep, true, 0.f, dk);
-            store_row<kCols>(tdV + co, have && !keep, true, 0.f, dv);
-          } else {
-            store_row<kCols>(tdK + co, have, zero, a.scale, dk);
-            store_row<kCols>(tdV + co, have, zero, 1.f, dv);
-          }
+          // every product that reads K and V is done: their memory takes the rows (zeros
+          // for rows with room but not in use, whatever their accumulators hold)
+          uint8_t *const tk = sgen + (sK - sbase), *const tv = sgen + (sV - sbase);
+          const int ch0 = half * (kCols / 8);
+          put_row<D, kCols>(tdK + co, zero || !keep, a.scale, tk, row, ch0);
+          put_row<D, kCols>(tdV + co, zero || !keep, 1.f, tv, row, ch0);
+          flush_rows<D, kCols>(tk, 32 * q, have ? a.dk + r * a.sdk[0] + kvh * a.sdk[1] + half * kCols : nullptr, ch0);
+          flush_rows<D, kCols>(tv, 32 * q, have ? a.dv + r * a.sdv[0] + kvh * a.sdv[1] + half * kCols : nullptr, ch0);
         }
       }
     }
@@ -447,7 +436,8 @@ __device__ __forceinline__ void packed_keys_cta(const CUtensorMap &tmQ, const CU
 
 // The kind that keeps dQ, `block` of `blocks`.
 template <int D>
-__device__ __forceinline__ void packed_queries_cta(const CUtensorMap &tmK, const CUtensorMap &tmV, const PackedArgs &a,
+__device__ __forceinline__ void packed_queries_cta(const CUtensorMap &tmQ, const CUtensorMap &tmK, const CUtensorMap &tmV,
+                                                   const CUtensorMap &tmO, const PackedArgs &a,
                                                    const uint32_t limit, int block, int blocks) {
   using T = Tile<D>;
   extern __shared__ __align__(1024) uint8_t sgen[];
@@ -470,6 +460,7 @@ __device__ __forceinline__ void packed_queries_cta(const CUtensorMap &tmK, const
   const uint32_t b_kedge = sBar + 8u * 14;  // the last tile of K, of V landed
   const uint32_t b_vedge = sBar + 8u * 15;
   const uint32_t b_drain = sBar + 8u * 16;
+  const uint32_t b_qo = sBar + 8u * 17;     // Q and dO landed (the copies, or an arrival per elementwise warp)
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sgen + (sBar - sbase) + 8 * 20);
   volatile int *abort = reinterpret_cast<volatile int *>(sgen + (sBar - sbase) + 8 * 20 + 4);
 
@@ -485,6 +476,7 @@ __device__ __forceinline__ void packed_queries_cta(const CUtensorMap &tmK, const
   const int r0 = (int)(piece * 128);
   const int rows = (int)min((int64_t)128, nrows - r0);
   const int nsteps = (s.visible(a, (r0 + rows - 1) / a.group) + 127) >> 7;
+  const bool q_copy = 128 % a.group == 0;
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < 3; ++i) {
@@ -501,6 +493,7 @@ __device__ __forceinline__ void packed_queries_cta(const CUtensorMap &tmK, const
     tc::mbar_init(b_kedge, 1);
     tc::mbar_init(b_vedge, 1);
     tc::mbar_init(b_drain, 1);
+    tc::mbar_init(b_qo, q_copy ? 1 : 8);
     *abort = 0;
     tc::fence_barrier_init();
   }
@@ -508,16 +501,6 @@ __device__ __forceinline__ void packed_queries_cta(const CUtensorMap &tmK, const
     tc::tmem_alloc(smem_u32(tmem_slot), 512);
     tc::tmem_relinquish();
   }
-  for (int i = threadIdx.x; i < 128 * (D / 8); i += kPbThreads) {
-    const int r = i / (D / 8), ch = i % (D / 8);
-    const bool have = r < rows;
-    const int fr = r0 + (have ? r : 0), tok = fr / a.group, head = kvh * a.group + fr - tok * a.group;
-    cp_async16_or_zero(sQ + T::off(r, ch), a.q + (int64_t)(s.q0 + tok) * a.sq[0] + (int64_t)head * a.sq[1] + ch * 8, have);
-    cp_async16_or_zero(sO + T::off(r, ch), a.dout + (int64_t)(s.q0 + tok) * a.sdo[0] + (int64_t)head * a.sdo[1] + ch * 8, have);
-  }
-  cp_async_commit();
-  cp_async_wait<0>();
-  fence_async_smem();
   tc::tc_fence_before();
   __syncthreads();
   tc::tc_fence_after();
@@ -527,6 +510,15 @@ __device__ __forceinline__ void packed_queries_cta(const CUtensorMap &tmK, const
 
   if (warp == 0) {
     // ------------------------------------------------------------ producer
+    if (lane == 0 && q_copy && nsteps > 0) {
+      // (rows behind the sequence's last one: as in the forward)
+      tc::mbar_expect_tx(b_qo, 2 * T::kBytes);
+#pragma unroll
+      for (int c = 0; c < T::kAtoms; ++c) {
+        tma_load_3d(sQ + c * T::kAtom, &tmQ, 64 * c, kvh * a.group, s.q0 + r0 / a.group, b_qo);
+        tma_load_3d(sO + c * T::kAtom, &tmO, 64 * c, kvh * a.group, s.q0 + r0 / a.group, b_qo);
+      }
+    }
     int nk = 0, nv = 0, kedge = 0, vedge = 0;
     for (int n = 0; n < nsteps; ++n) {
       const int valid = s.lk - 128 * n, ki = n % 3, vi = n & 1;
@@ -572,6 +564,7 @@ __device__ __forceinline__ void packed_queries_cta(const CUtensorMap &tmK, const
         tc::mbar_wait(b_vfull(k & 1), (uint32_t)(k >> 1) & 1u, &no_abort, limit);
       if (kedge) tc::mbar_wait(b_kedge, 0, &no_abort, limit);
       if (vedge) tc::mbar_wait(b_vedge, 0, &no_abort, limit);
+      if (q_copy && nsteps > 0) tc::mbar_wait(b_qo, 0, &no_abort, limit);
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
@@ -601,7 +594,7 @@ __device__ __forceinline__ void packed_queries_cta(const CUtensorMap &tmK, const
         rows_by_rows(tDP, dO, sV(n & 1), b_dp);
         tc::mma_commit(b_vempty(n & 1));
       };
-      bool ok = scores(0) && landed_v(0);
+      bool ok = wait(b_qo, 0) && scores(0) && landed_v(0);
       if (ok) {
         dprob(0);
         ok = nsteps < 2 || scores(1);
@@ -634,6 +627,17 @@ __device__ __forceinline__ void packed_queries_cta(const CUtensorMap &tmK, const
     const float4 d4 = make_float4(delta, delta, delta, delta);
     const float cS = a.scale_log2;
     bool ok = true;
+    if (!q_copy) {
+      const int t = (int)threadIdx.x - 64;
+      if (nsteps > 0) {
+        load_rows_async<D>(sQ, a.q, a.sq, s.q0, kvh * a.group, a.group, r0, rows, 128, t, 256);
+        load_rows_async<D>(sO, a.dout, a.sdo, s.q0, kvh * a.group, a.group, r0, rows, 128, t, 256);
+      }
+      cp_async_commit();
+      cp_async_wait<0>();
+      fence_async_smem();
+      warp_arrive(b_qo);
+    }
     for (int n = 0; n < nsteps; ++n) {
       if (!warp_wait(b_s(n & 1), (uint32_t)(n >> 1) & 1u, abort, limit)) {
         ok = false;
@@ -676,8 +680,10 @@ __device__ __forceinline__ void packed_queries_cta(const CUtensorMap &tmK, const
       if (ok) {
         tc::tc_fence_after();
         constexpr int kCols = D / 2;
-        store_row<kCols>(tdQ + lane_off + (uint32_t)(half * kCols), have, nsteps == 0, a.scale,
-                         a.dq + (int64_t)(s.q0 + tok) * a.sdq[0] + (int64_t)head * a.sdq[1] + half * kCols);
+        uint8_t *const tile = sgen + (sQ - sbase);      // every product that reads Q is done
+        const int ch0 = half * (kCols / 8);
+        put_row<D, kCols>(tdQ + lane_off + (uint32_t)(half * kCols), nsteps == 0, a.scale, tile, row, ch0);
+        flush_rows<D, kCols>(tile, 32 * q, have ? a.dq + (int64_t)(s.q0 + tok) * a.sdq[0] + (int64_t)head * a.sdq[1] + half * kCols : nullptr, ch0);
       }
     }
   }
@@ -699,7 +705,7 @@ __global__ void __launch_bounds__(kPbThreads, 1)
                          const PackedArgs a, const PackedParts parts, const uint32_t limit, const int key_blocks) {
   const int block = (int)blockIdx.x;
   if (block < key_blocks) packed_keys_cta<D>(tmQ, tmK, tmV, tmO, a, parts, limit, block);
-  else packed_queries_cta<D>(tmK, tmV, a, limit, block - key_blocks, (int)gridDim.x - key_blocks);
+  else packed_queries_cta<D>(tmQ, tmK, tmV, tmO, a, limit, block - key_blocks, (int)gridDim.x - key_blocks);
 }
 
 // Adds the shares of walks that were cut (see KeyWalk), in order: one CTA per (128

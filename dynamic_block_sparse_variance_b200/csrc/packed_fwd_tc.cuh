@@ -101,20 +101,20 @@ __device__ __forceinline__ void load_rows_async(uint32_t tile, const __nv_bfloat
   }
 }
 
-// A warp's 32 rows of D bf16, which it has put into rows [row0, row0 + 32) of a tile in
-// shared memory, to their places in global memory, whole rows at a time (straight
-// from the registers, a row per lane, every store would touch 32 rows).  dst: this
-// lane's row, nullptr for none.
-template <int D>
-__device__ __forceinline__ void flush_rows(const uint8_t *tile, int row0, __nv_bfloat16 *dst) {
-  constexpr int CH = D / 8;
+// A warp's 32 rows of COLS bf16, which it has put into rows [row0, row0 + 32) of a tile
+// of D columns in shared memory, from 16-byte piece ch0 on, to their places in global
+// memory, whole rows at a time (straight from the registers, a row per lane, every
+// store would touch 32 rows).  dst: where this lane's row goes, nullptr for none.
+template <int D, int COLS = D>
+__device__ __forceinline__ void flush_rows(const uint8_t *tile, int row0, __nv_bfloat16 *dst, int ch0 = 0) {
+  constexpr int CH = COLS / 8;
   const int lane = threadIdx.x & 31, ch = lane % CH;
   __syncwarp();
 #pragma unroll 4
   for (int i = 0; i < CH; ++i) {      // 32 / CH rows at a time
     const int r = i * (32 / CH) + lane / CH;
     __nv_bfloat16 *const p = reinterpret_cast<__nv_bfloat16 *>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(dst), r));
-    const uint4 w = *reinterpret_cast<const uint4 *>(tile + Tile<D>::off(row0 + r, ch));
+    const uint4 w = *reinterpret_cast<const uint4 *>(tile + Tile<D>::off(row0 + r, ch0 + ch));
     if (p) *reinterpret_cast<uint4 *>(p + ch * 8) = w;
   }
   __syncwarp();
