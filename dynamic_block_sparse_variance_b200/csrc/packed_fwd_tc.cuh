@@ -436,6 +436,10 @@ __global__ void __launch_bounds__(64 + 128 * NG, 3 - NG)
       if (steps > 0) {
         if (!__all_sync(0xffffffffu, tc::mbar_wait(b_drain, 0, abort, limit))) ok = false;
         tc::tc_fence_after();
+      } else if (t0 < tend) {
+        // no key for this tile, some for the other: Q comes in for both, and the zeros
+        // below go into its place
+        if (!__all_sync(0xffffffffu, tc::mbar_wait(b_q, 0, abort, limit))) ok = false;
       }
       if (ok) {
         const float inv = l_run > 0.f ? 1.f / l_run : 0.f;

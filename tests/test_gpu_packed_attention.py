@@ -90,6 +90,29 @@ def test_forward_and_backward(shape, causal, dim):
     _check(q, k, v, dout, qo, ko, causal, 0.0, None, att, o, grads, name, average=True)
 
 
+@pytest.mark.parametrize("dim,heads,kv", [(128, 2, 2), (128, 4, 1), (64, 3, 1)])
+def test_a_tile_without_keys_beside_one_that_has_some(dim, heads, kv):
+    """Causal with more queries than keys, enough keys for pairs of 128-row tiles, and a first seen key in the
+    second tile of a pair: the first tile's zeros and its queries, which nobody reads, go to the same memory."""
+    gen = torch.Generator().manual_seed(dim + heads)
+    group = heads // kv
+    blind = (256 + 128 + group) // group            # rows up to 128 .. 256 + a token of the second pair see nothing
+    lq, lk = [600 + blind, 520, 640 + blind], [600, 520, 640]
+    qo, ko = ref.offsets(lq), ref.offsets(lk)
+    q, dout = (_randn(gen, qo[-1], heads, dim) for _ in range(2))
+    k, v = (_randn(gen, ko[-1], kv, dim) for _ in range(2))
+    att = PackedAttention(heads, kv, dim)
+    first = None
+    for _ in range(50):
+        o = att.forward(q, k, v, _ints(qo), _ints(ko))
+        P.prism_device_status()
+        for s in (qo[0], qo[2]):
+            assert (o[s:s + blind] == 0).all() and torch.isneginf(att.lse[:, s:s + blind]).all()
+        first = o if first is None else first
+        assert torch.equal(o, first)
+    _check(q, k, v, dout, qo, ko, True, 0.0, None, att, o, att.backward(dout), "blind rows", average=True)
+
+
 @pytest.mark.parametrize("dim,heads,kv", [(128, 4, 2), (64, 6, 2)])
 def test_what_lies_outside_the_sequences_reaches_nothing(dim, heads, kv):
     """NaN before, between and behind the sequences' rows and behind k_used; rows outside stay as they were."""
