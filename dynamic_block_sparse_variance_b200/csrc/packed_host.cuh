@@ -186,6 +186,7 @@ static int launch_packed_bwd(const prism_packed_params *p, const PackedArgs &a, 
                              float *lse2, cudaStream_t st) {
   const int64_t dummy[2] = {D, D};
   const bool keys = p->k_rows > 0, rows = p->q_rows > 0;
+  if (!keys && !rows) return PRISM_OK;
   const int tt = 128 / a.group;     // tokens per streamed query tile
   const void *any = rows ? (const void *)a.q : a.k;
   CUtensorMap tq, to, tk, tv;
@@ -201,7 +202,6 @@ static int launch_packed_bwd(const prism_packed_params *p, const PackedArgs &a, 
   const int64_t key_tiles = keys ? parts.tiles : 0, key_blocks = key_tiles * parts.splits;
   const int64_t blocks = key_blocks + (rows ? slot_bound(p->q_rows, p->seqs, a.group, 128) * a.kv_heads : 0);
   if (blocks > 0x7fffffffLL) return fail(PRISM_EINVAL, "packed: too many rows");
-  if (blocks == 0) return PRISM_OK;
   cudaFuncSetAttribute(packed_bwd_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, kPbSmem<D>);
   PRISM_TRACED("packed_bwd_tc_kernel", st, packed_bwd_tc_kernel<D><<<(unsigned)blocks, kPbThreads, kPbSmem<D>, st>>>(tq, tk, tv, to, a, parts, wait_limit(), (int)key_blocks));
   if (parts.splits > 1 && keys)

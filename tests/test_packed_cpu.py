@@ -138,6 +138,11 @@ def test_packed_pointers_refused(lib):
     assert lib.prism_packed_attn_fwd(ctypes.byref(empty), *[None] * 10, 0, None) == P.PRISM_OK
 
 
+def test_packed_backward_of_nothing_touches_no_device(lib):
+    empty = _pp(q_rows=0, k_rows=0)
+    assert lib.prism_packed_attn_bwd(ctypes.byref(empty), *[None] * 14, 0, None) == P.PRISM_OK
+
+
 @pytest.mark.parametrize("bad,what", [
     (dict(rows=-1), "rows"), (dict(seqs=0), "seqs"), (dict(channels=12), "channels"), (dict(channels=8200), "channels"),
     (dict(stream_dtype=2), "dtypes"), (dict(branch_dtype=-1), "dtypes"), (dict(param_dtype=5), "dtypes"),
