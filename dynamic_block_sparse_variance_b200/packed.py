@@ -84,6 +84,18 @@ def _heads_view(shape, stride, heads, dim, name):
     return n, seqs, row, head
 
 
+def _used_here(at, stream, tensors):
+    """The current raw stream of device `at`. Where it is not `stream`, the one that `tensors` were written on, the
+    allocator learns that they are read here too: the next forward() lets go of them, maybe before this one is through."""
+    now = _raw_stream(at)
+    if now != stream:
+        here = torch.cuda.current_stream(at)
+        for t in tensors:
+            if t is not None:
+                t.record_stream(here)
+    return now
+
+
 class _FwdPlan:
     __slots__ = ("p", "q_rows", "ws", "offsets")
 
@@ -167,9 +179,10 @@ class PackedAttention:
         lse = q.new_empty((self.heads, plan.q_rows), dtype=torch.float32)
         o_res = q.new_empty((plan.q_rows, self.heads, self.head_dim)) if self.training else None
         ws = q.new_empty(plan.ws, dtype=torch.uint8) if plan.ws else None
-        P.prism_packed_attn_fwd(plan.p, q, k, v, q_offsets, k_offsets, k_used, out, o_res, lse, ws, _raw_stream(at))
+        stream = _raw_stream(at)
+        P.prism_packed_attn_fwd(plan.p, q, k, v, q_offsets, k_offsets, k_used, out, o_res, lse, ws, stream)
         self.lse = lse
-        self._saved = (key, plan.p, q, k, v, out, o_res, lse, q_offsets, k_offsets, k_used) if self.training else None
+        self._saved = (key, plan.p, stream, q, k, v, out, o_res, lse, q_offsets, k_offsets, k_used) if self.training else None
         return out
 
     def _backward_plan(self, p, shapes, strides):
@@ -183,7 +196,7 @@ class PackedAttention:
     def backward(self, dout, dq=None, dk=None, dv=None):
         """Gradients (dQ, dK, dV) of the last forward(), shaped like q, k and v."""
         _need(self._saved is not None, "backward() needs a forward() with training=True before it")
-        key, p, q, k, v, o, o_res, lse, q_offsets, k_offsets, k_used = self._saved
+        key, p, stream, q, k, v, o, o_res, lse, q_offsets, k_offsets, k_used = self._saved
         at = q.get_device()
         if at != torch.cuda.current_device():
             with torch.cuda.device(at):
@@ -202,8 +215,8 @@ class PackedAttention:
         dk = _like(k) if dk is None else dk
         dv = _like(v) if dv is None else dv
         ws = q.new_empty(n, dtype=torch.uint8) if n else None
-        P.prism_packed_attn_bwd(bp, q, k, v, o, o_res, dout, lse, q_offsets, k_offsets, k_used, dq, dk, dv, ws,
-                                _raw_stream(at))
+        here = _used_here(at, stream, self._saved[3:])
+        P.prism_packed_attn_bwd(bp, q, k, v, o, o_res, dout, lse, q_offsets, k_offsets, k_used, dq, dk, dv, ws, here)
         return dq, dk, dv
 
 
@@ -327,10 +340,10 @@ class BlockNorm:
         if y_norms is not None:
             _need(y_norms.dtype == torch.float32 and y_norms.is_contiguous() and y_norms.numel() == plan.p.rows,
                   f"y_norms must be {plan.p.rows} contiguous floats")
-        P.prism_block_norm_fwd(plan.p, x, y, offsets, post_weight, gate, weight, scale, shift, x_out, h, y_norms,
-                               _raw_stream(at))
+        stream = _raw_stream(at)
+        P.prism_block_norm_fwd(plan.p, x, y, offsets, post_weight, gate, weight, scale, shift, x_out, h, y_norms, stream)
         kept = x if y is None else x_out
-        self._saved = (key, plan, kept, y, offsets, params) if self.training else None
+        self._saved = (key, plan, stream, kept, y, offsets, params) if self.training else None
         return kept, h
 
     def _backward_plan(self, plan, kept, y, given):
@@ -350,7 +363,7 @@ class BlockNorm:
         shaped and typed like what they belong to. ``dx_out``: the gradient that reaches the residual stream behind
         the block (None: zero)."""
         _need(self._saved is not None, "backward() needs a forward() with training=True before it")
-        key, plan, kept, y, offsets, params = self._saved
+        key, plan, stream, kept, y, offsets, params = self._saved
         at = kept.get_device()
         if at != torch.cuda.current_device():
             with torch.cuda.device(at):
@@ -367,6 +380,6 @@ class BlockNorm:
         post_weight, gate, weight, scale, shift = params
         grads = [None if t is None or (y is None and i < 2) else _like(t) for i, t in enumerate(params)]
         ws = kept.new_empty(plan.ws, dtype=torch.uint8)
-        P.prism_block_norm_bwd(p, kept, y, offsets, post_weight, gate, weight, scale, dh, dx_out, dx, dy, *grads, ws,
-                               _raw_stream(at))
+        here = _used_here(at, stream, (kept, y, offsets, *params))
+        P.prism_block_norm_bwd(p, kept, y, offsets, post_weight, gate, weight, scale, dh, dx_out, dx, dy, *grads, ws, here)
         return {"dx": dx, "dy": dy, **{"d" + n: g for n, g in zip(_PARAMS, grads)}}

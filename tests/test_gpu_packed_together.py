@@ -176,3 +176,33 @@ def test_long_walks_are_cut_the_same_way_every_time():
             assert (np.abs(g[lo:hi] - want[n][lo:hi]) <= bound[n][lo:hi]).all(), (n, causal)
             if n != "dq":
                 assert (g[:lo] == 7.0).all() and (g[hi:] == 7.0).all()
+
+
+def test_backward_on_another_stream_keeps_what_the_forward_left():
+    """The next forward, on the first stream, lets go of what a late backward on another stream still reads; what
+    is allocated then must not be that memory."""
+    gen = torch.Generator().manual_seed(9)
+    q, k, v, dout = (torch.randn(900, 4, 128, generator=gen).to(BF16).cuda() for _ in range(4))
+    x, y, dh = (torch.randn(900, 512, generator=gen).to(BF16).cuda() for _ in range(3))
+    att, norm = PackedAttention(4, 4, 128), BlockNorm(512, post="rms")
+    att.forward(q, k, v)
+    norm.forward(x, y)
+    want = [*att.backward(dout), *(norm.backward(dh)[n] for n in ("dx", "dy"))]
+    torch.cuda.synchronize()
+    a, b = torch.cuda.Stream(), torch.cuda.Stream()
+    for _ in range(3):
+        with torch.cuda.stream(a):
+            att.forward(q, k, v)
+            norm.forward(x, y)
+        b.wait_stream(a)
+        with torch.cuda.stream(b):
+            torch.cuda._sleep(20_000_000)           # some 10 ms: the backward starts after all that follows
+            got = [*att.backward(dout), *(norm.backward(dh)[n] for n in ("dx", "dy"))]
+        with torch.cuda.stream(a):
+            att.forward(q, k, v)
+            norm.forward(x, y)
+            for shape, dtype in (((900, 4, 128), BF16), ((4, 900), torch.float32), ((900, 512), BF16)) * 4:
+                torch.full(shape, float("nan"), dtype=dtype, device="cuda")
+        torch.cuda.synchronize()
+        P.prism_device_status()
+        assert all(torch.equal(g, w) for g, w in zip(got, want))
