@@ -23,6 +23,19 @@ static bool fill_strides(const int64_t in[2], int64_t rows, int heads, int D, bo
   return rows_outer || heads_outer;
 }
 
+// Whether a written tensor begins where another one does (what else overlaps is the caller's to see: slices
+// of one buffer interleave without sharing an element).
+static bool same_start(std::initializer_list<const void *> written, std::initializer_list<const void *> read) {
+  for (auto w = written.begin(); w != written.end(); ++w) {
+    if (!*w) continue;
+    for (auto v = written.begin(); v != w; ++v)
+      if (*v == *w) return true;
+    for (const void *r : read)
+      if (r == *w) return true;
+  }
+  return false;
+}
+
 static bool even_split(int64_t rows, int seqs) { return rows % seqs == 0; }
 
 static int check_packed(const prism_packed_params *p) {
@@ -215,6 +228,18 @@ static bool norm_row_stride(int64_t in, int C, int64_t *out) {
   *out = in ? in : C;
   return in == 0 || (in >= C && in % 8 == 0 && in < ((int64_t)1 << 40));
 }
+// A row's copies have landed before the row is written, so an output may begin where an input does if its
+// rows lie the same way: the same type and row stride.
+struct NormInput {
+  const void *p;
+  int64_t stride;
+  bool same_type;
+};
+static bool in_place(const void *out, int64_t stride, std::initializer_list<NormInput> in) {
+  for (const NormInput &i : in)
+    if (i.p == out && !(i.same_type && i.stride == stride)) return false;
+  return true;
+}
 static bool is_float_type(int t) { return t == PRISM_BF16 || t == PRISM_F32; }
 
 static int check_norm(const prism_norm_params *p) {
@@ -391,6 +416,8 @@ int prism_packed_attn_fwd(const prism_packed_params *p, const void *q, const voi
   const size_t need = PackedFwdWs(p).total;
   if (need && (!workspace || ws_bytes < need || !aligned16(workspace)))
     return fail(PRISM_EINVAL, "packed: workspace missing, misaligned or below prism_packed_workspace_size");
+  if (same_start({o, o_res, lse}, {q, p->k_rows ? k : nullptr, p->k_rows ? v : nullptr}))
+    return fail(PRISM_EINVAL, "packed: an output must not take the place of an input or of another output");
   cudaStream_t st = as_stream(stream);
   uint8_t *ws = static_cast<uint8_t *>(workspace);
   return p->head_dim == 128 ? launch_packed_fwd<128>(p, a, ws, st) : launch_packed_fwd<64>(p, a, ws, st);
@@ -417,6 +444,9 @@ int prism_packed_attn_bwd(const prism_packed_params *p, const void *q, const voi
   const PackedBwdWs w(p);
   if (w.total && (!workspace || ws_bytes < w.total || !aligned16(workspace)))
     return fail(PRISM_EINVAL, "packed: workspace missing, misaligned or below prism_packed_workspace_size");
+  if (p->q_rows && p->k_rows ? same_start({dq, dk, dv}, {q, k, v, o, o_res, dout, lse})
+                             : p->q_rows ? same_start({dq}, {q, o, o_res, dout, lse}) : p->k_rows && same_start({dk, dv}, {k, v}))
+    return fail(PRISM_EINVAL, "packed: an output must not take the place of an input or of another output");
   uint8_t *ws = static_cast<uint8_t *>(workspace);
   float *delta = reinterpret_cast<float *>(ws + w.delta), *lse2 = reinterpret_cast<float *>(ws + w.lse2);
   a.o = static_cast<__nv_bfloat16 *>(const_cast<void *>(o));
@@ -447,6 +477,10 @@ int prism_block_norm_fwd(const prism_norm_params *p, const void *x, const void *
   if (!y && y_norms) return fail(PRISM_EINVAL, "block_norm: y_norms needs y");
   for (const void *t : {x, y, (const void *)x_out, (const void *)h})
     if (!aligned16(t)) return fail(PRISM_EINVAL, "block_norm: tensors must be 16-byte aligned");
+  const bool xt = p->stream_dtype == p->branch_dtype;      // x and x_out have the types of y and h
+  if ((y && h && same_start({x_out, h}, {})) || (y && !in_place(x_out, a.sxo, {{x, a.sx, true}, {y, a.sy, xt}})) ||
+      (h && !in_place(h, a.sh, {{x, a.sx, xt}, {y, a.sy, true}})))
+    return fail(PRISM_EINVAL, "block_norm: an output takes an input's place only with its type and row stride, and never another output's");
   a.x = x;
   a.y = y;
   a.x_out = y ? x_out : nullptr;
@@ -488,6 +522,11 @@ int prism_block_norm_bwd(const prism_norm_params *p, const void *x_out, const vo
   const size_t need_ws = (size_t)w.slots * w.groups * 3 * p->channels * 4;
   if (!workspace || ws_bytes < need_ws || !aligned16(workspace))
     return fail(PRISM_EINVAL, "block_norm: workspace missing, misaligned or below prism_block_norm_workspace_size");
+  const bool xt = p->stream_dtype == p->branch_dtype;
+  if (p->rows && (same_start({dx, y ? dy : nullptr}, {}) ||
+                  !in_place(dx, a.sdx, {{x_out, a.sxo, true}, {dx_out, a.sdxo, true}, {dh, a.sdh, xt}, {y, a.sy, xt}}) ||
+                  (y && !in_place(dy, a.sdy, {{x_out, a.sxo, xt}, {dx_out, a.sdxo, xt}, {dh, a.sdh, true}, {y, a.sy, true}}))))
+    return fail(PRISM_EINVAL, "block_norm: an output takes an input's place only with its type and row stride, and never another output's");
   a.unit = w.unit;
   a.wpr = w.wpr;
   a.groups = w.groups;

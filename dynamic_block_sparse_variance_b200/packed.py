@@ -110,7 +110,7 @@ class PackedAttention:
     keys, the one before it all but the last, and so on; a query that sees no key gets 0 (and lse -inf).
     ``k_used`` (device int32): only so many of each sequence's key rows are in use, as in a cache with room.
     With ``training`` forward() keeps what backward() needs: its inputs and outputs (not copies; leave
-    them unchanged until then) and the rounding residual of O. Rows outside every sequence are left as
+    them unchanged until then) and the rounding residual of O. No output may overlap an input. Rows outside every sequence are left as
     they were; pass ``out`` (and dq, dk, dv) to say what that is. Calls run on the device of q and its
     current stream.
     """
@@ -255,8 +255,9 @@ class BlockNorm:
     block's output) are [rows, channels] or [sequences, rows, channels], bf16 or f32 each; the weights are
     [channels], gate, scale and shift [channels] or [1, channels] (shared), or [sequences, channels] with
     ``offsets`` saying which rows are whose; all of these have one type, bf16 or f32. Every parameter may be
-    left out. With ``training`` forward() keeps what backward() needs (not copies). Rows outside every sequence
-    are left as they were. Calls run on the device of x and its current stream.
+    left out. With ``training`` forward() keeps what backward() needs: y, x_out and the parameters (not copies; leave
+    them unchanged until then). Outputs may take the place of inputs of the same type and strides: x_out that of x, dx
+    that of dx_out, dy that of dh and, without training, h that of y. Rows outside every sequence are left as they were. Calls run on the device of x and its current stream.
     """
 
     def __init__(self, channels, *, post="none", pre="rms", eps=1e-6, alpha=1.0, training=True):
@@ -328,7 +329,9 @@ class BlockNorm:
         _same_device(at, y, x_out, h, y_norms, *params)
         n_off = _index(offsets, at, "offsets")
         if y is None:
-            x_out = None
+            _need(x_out is None, "x_out belongs to a y")
+        elif self.training and h is not None:
+            _need(h.data_ptr() != y.data_ptr() or not h.numel(), "h must not take the place of y, which backward() needs")
         layouts = (_layout(x), _layout(y), _layout(x_out), _layout(h), h_dtype, n_off,
                    (_layout(post_weight), _layout(gate), _layout(weight), _layout(scale), _layout(shift)))
         key = (self.channels, self.post, self.pre, self.eps, self.alpha, layouts)

@@ -373,6 +373,8 @@ int prism_packed_workspace_size(const prism_packed_params *p, int kind, size_t *
  * Values within a sequence have to be finite: a masked (future) key's value
  * is multiplied by zero.  What lies outside the sequences, or behind k_used, does
  * not reach any result.  Results do not change from run to run.
+ * No output may overlap an input or another output (here and in the backward;
+ * where two begin at one address the call is refused).
  */
 int prism_packed_attn_fwd(const prism_packed_params *p, const void *q, const void *k, const void *v,
                           const int32_t *q_off, const int32_t *k_off, const int32_t *k_used, void *o,
@@ -432,6 +434,10 @@ typedef struct {
  *   y_norms   out, nullable: [rows] float ||y_n||_2, the indicator's audio
  *             input when y is the audio-to-video cross-attention's output
  *             (Method §1; what prism_audio_norms computes in a pass of its own)
+ * An output may take the place of an input of its type and row stride (x_out that
+ * of x, h that of y; in the backward dx that of dx_out, dy that of dh): a row is
+ * read before it is written.  Any other overlap is the caller's mistake; where it
+ * shows in the addresses alone the call is refused.
  */
 int prism_block_norm_fwd(const prism_norm_params *p, const void *x, const void *y, const int32_t *off,
                          const void *post_weight, const void *gate, const void *weight, const void *scale,

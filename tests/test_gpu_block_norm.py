@@ -176,6 +176,37 @@ def test_strided_tensors_and_a_modulation_tensor():
     assert all((t[:, c:] == 9.0).all() for t in outs.values())
 
 
+@pytest.mark.parametrize("c", [256, 1536, 2056, 4104, 8192])
+def test_in_place(c):
+    """x_out over x, h over y, dx over dx_out, dy over dh: the same bits as in tensors of their own."""
+    a = _inputs(1200, c, 1, "bf16", "bf16", "f32", "shared", seed=c)
+    kw = {n: a[n] for n in NAMES}
+    norm = BlockNorm(c, post="rms", pre="layer", alpha=0.9)
+    x_out, h = norm.forward(a["x"], a["y"], **kw)
+    g = norm.backward(a["dh"], a["dx_out"])
+    x = a["x"].clone()
+    over, h2 = norm.forward(x, a["y"], x_out=x, **kw)
+    assert over is x and torch.equal(x, x_out) and torch.equal(h2, h)
+    dh, dxo = a["dh"].clone(), a["dx_out"].clone()
+    g2 = norm.backward(dh, dxo, dx=dxo, dy=dh)
+    assert g2["dx"] is dxo and g2["dy"] is dh
+    for n in g:
+        assert torch.equal(g2[n], g[n]), n
+    x, y = a["x"].clone(), a["y"].clone()
+    BlockNorm(c, post="rms", pre="layer", alpha=0.9, training=False).forward(x, y, x_out=x, h=y, **kw)
+    P.prism_device_status()
+    assert torch.equal(x, x_out) and torch.equal(y, h)
+
+
+def test_refused_places():
+    norm = BlockNorm(64)
+    x, y = (torch.zeros(6, 64, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    for args, kw in (((x, y), dict(h=y)), ((x,), dict(x_out=y)), ((x, y), dict(x_out=x, h=x))):
+        with pytest.raises(P.PrismError) as e:
+            norm.forward(*args, **kw)
+        assert e.value.code == P.PRISM_EINVAL
+
+
 def test_rows_outside_the_sequences_stay_as_they_were():
     off = np.array([4, 10, 10, 25], np.int32)
     a = _inputs(40, 96, 3, "bf16", "bf16", "bf16", "per")

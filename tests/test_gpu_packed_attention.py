@@ -294,6 +294,25 @@ def test_refusals_on_the_device():
         assert e.value.code == P.PRISM_EINVAL
 
 
+def test_outputs_on_other_tensors_refused():
+    q = torch.zeros(10, 4, 64, dtype=BF16, device="cuda")
+    att = PackedAttention(4, 4, 64)
+    for args, kw in (((q, q, q), dict(out=q)), ((torch.zeros_like(q), q, torch.zeros_like(q)), dict(out=q))):
+        with pytest.raises(P.PrismError) as e:
+            att.forward(*args, **kw)
+        assert e.value.code == P.PRISM_EINVAL
+    o = att.forward(q, q, q)            # one tensor may be read three times
+    g = torch.ones_like(q)
+    for args in ((g, g), (g, o), (g, None, q), (g, None, torch.zeros_like(q), o)):
+        with pytest.raises(P.PrismError) as e:
+            att.backward(*args)
+        assert e.value.code == P.PRISM_EINVAL
+    d = torch.zeros_like(q)
+    with pytest.raises(P.PrismError):
+        att.backward(g, None, d, d)
+    assert all(torch.isfinite(t.float()).all() for t in att.backward(g))
+
+
 def test_no_rows():
     q, k = torch.zeros(0, 4, 64, dtype=BF16, device="cuda"), torch.zeros(6, 2, 64, dtype=BF16, device="cuda")
     att = PackedAttention(4, 2, 64)

@@ -143,6 +143,39 @@ def test_packed_backward_of_nothing_touches_no_device(lib):
     assert lib.prism_packed_attn_bwd(ctypes.byref(empty), *[None] * 14, 0, None) == P.PRISM_OK
 
 
+def _spread(n, **same):
+    """n pointers 1 MB apart; `same`: position -> position whose pointer it takes."""
+    a = [ctypes.c_void_p(0x100000 * (i + 1)) for i in range(n)]
+    for i, j in same.items():
+        a[int(i[1:])] = a[j]
+    return a
+
+
+@pytest.mark.parametrize("i,j", [(6, 0), (6, 1), (6, 2), (7, 0), (7, 6), (8, 6)])      # o, o_res, lse on q, k, v, o
+def test_packed_forward_outputs_on_other_tensors_refused(lib, i, j):
+    assert lib.prism_packed_attn_fwd(ctypes.byref(_pp()), *_spread(10, **{f"_{i}": j}), 1 << 40, None) == P.PRISM_EINVAL
+    assert b"take the place" in lib.prism_last_error()
+
+
+@pytest.mark.parametrize("i,j", [(10, 0), (10, 3), (10, 5), (11, 1), (12, 2), (12, 11), (11, 10)])
+def test_packed_backward_outputs_on_other_tensors_refused(lib, i, j):
+    # q k v o o_res dout lse q_off k_off k_used dq dk dv workspace
+    assert lib.prism_packed_attn_bwd(ctypes.byref(_pp()), *_spread(14, **{f"_{i}": j}), 1 << 40, None) == P.PRISM_EINVAL
+    assert b"take the place" in lib.prism_last_error()
+
+
+def test_norm_outputs_on_other_tensors_refused(lib):
+    # x y off post_weight gate weight scale shift x_out h y_norms; stream and branch bf16
+    for p, i, j in ((_np(), 9, 8), (_np(x_out_row_stride=128), 8, 0), (_np(h_row_stride=72), 9, 1),
+                    (_np(stream_dtype=1), 9, 0), (_np(branch_dtype=1), 8, 1)):
+        assert lib.prism_block_norm_fwd(ctypes.byref(p), *_spread(11, **{f"_{i}": j}), None) == P.PRISM_EINVAL
+        assert b"an input's place" in lib.prism_last_error()
+    # x_out y off post_weight gate weight scale dh dx_out dx dy ...
+    for p, i, j in ((_np(), 10, 9), (_np(dx_row_stride=72), 9, 8), (_np(dy_row_stride=72), 10, 7), (_np(stream_dtype=1), 9, 7)):
+        assert lib.prism_block_norm_bwd(ctypes.byref(p), *_spread(17, **{f"_{i}": j}), 1 << 40, None) == P.PRISM_EINVAL
+        assert b"an input's place" in lib.prism_last_error()
+
+
 @pytest.mark.parametrize("bad,what", [
     (dict(rows=-1), "rows"), (dict(seqs=0), "seqs"), (dict(channels=12), "channels"), (dict(channels=8200), "channels"),
     (dict(stream_dtype=2), "dtypes"), (dict(branch_dtype=-1), "dtypes"), (dict(param_dtype=5), "dtypes"),
