@@ -301,8 +301,9 @@ __global__ void __launch_bounds__(64 + 128 * NG, 3 - NG)
       constexpr uint32_t idO = tc::idesc_bf16(128, D, false, true);
       const int n_all = tend - t0, n_g[2] = {t1[0] - t0, t1[NG - 1] - t0};
       const uint64_t dQ[2] = {tc::sw128_desc(sQ(0), 16, 1024), tc::sw128_desc(sQ(NG - 1), 16, 1024)};
+      const uint64_t dK0 = tc::sw128_desc(sK(0), 16, 1024), dV0 = tc::sw128_desc(sV(0), T::kAtom, 1024);
       auto issue_s = [&](int n, int g) {
-        const uint64_t dK = tc::sw128_desc(sK(n % kStages), 16, 1024), dQg = dQ[g];
+        const uint64_t dK = dK0 + (uint64_t)((uint32_t)(n % kStages) * (2u * T::kBytes >> 4)), dQg = dQ[g];
         const uint32_t tSg = tS(g);
 #pragma unroll
         for (int k = 0; k < D / 16; ++k)
@@ -310,7 +311,7 @@ __global__ void __launch_bounds__(64 + 128 * NG, 3 - NG)
         tc::mma_commit(b_sfull(g));
       };
       auto issue_pv = [&](int n, int g) {
-        const uint64_t dV = tc::sw128_desc(sV(n % kStages), T::kAtom, 1024);
+        const uint64_t dV = dV0 + (uint64_t)((uint32_t)(n % kStages) * (2u * T::kBytes >> 4));
         const uint32_t tOg = tO(g), tPg = tS(g);
 #pragma unroll
         for (int k = 0; k < 8; ++k)
