@@ -11,14 +11,16 @@
 // bytes in flight do not depend on registers.  What sets the time otherwise is
 // the reductions: with a row spread over a whole CTA (8 columns a thread) every
 // statistic is a butterfly, a barrier and a table, about 1000 cycles of
-// dependent latency, and most instructions (61440 x 1536 forward: 208 us).  So
+// dependent latency, and most instructions (61440 x 1536 forward: 208 us, 145 us as
+// it is now, 5.2 TB/s, 0.79 of the measured copy rate).  So
 //   forward   a row belongs to one warp (2 to 4 beyond 2048 channels), which
 //             keeps it in registers; warps run on their own, without barriers
 //   backward  the column sums, three per column, want to stay in registers, so
 //             a row is spread over the CTA all the same, two rows at a time
 // (The backward with rows by warps for the statistics and columns by threads for
-// the results reads each row three times and was slower: 331 us against 233 at
-// 30011 x 2048.)
+// the results reads each row three times and was slower: 331 us against 233 then at
+// 30011 x 2048.  204 us now, 3.6 TB/s: what is left is the two exchanges of sums per
+// pair of rows, whose barriers 16 warps per SM hide only in part.)
 #pragma once
 
 #include "packed_common.cuh"
@@ -26,7 +28,6 @@
 
 namespace prism {
 
-constexpr int kBnMaxChannels = 8192;
 constexpr int kBnWarps = 16;          // forward
 constexpr int kBnMaxThreads = 512;    // backward
 constexpr int kBnMaxGroups = 8;       // rows of a CTA at a time, backward

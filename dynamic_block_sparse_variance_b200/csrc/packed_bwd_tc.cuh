@@ -15,6 +15,13 @@
 // saves two products but writes 64 KB of reductions per tile pair and gives dQ
 // whose last bits change from run to run.
 //
+// Measured (8192 tokens, 8 heads of 128, all pairs, bursts): 854 us, 805 TFLOP/s of
+// the algorithm's 5 products, 1127 of the 7, 0.68 of the bf16 rate measured with a
+// library product; 164 us at 7 packed causal sequences of 6144 tokens in all, 16 / 4
+// heads.  What bounds it is a tile's chain again (S, P, its product, dP, dS, its
+// product, in all 512 columns of tensor memory), and the operands that the products
+// read from shared memory (S and dP both of theirs, 64 KB per 128 x 128 x 128).
+//
 // P and dS enter their products rounded once to bf16, the type of dO, Q and K
 // (a product's operands have one type); everything else is fp32.
 //

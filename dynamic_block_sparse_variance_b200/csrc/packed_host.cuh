@@ -129,9 +129,14 @@ static uint32_t wait_limit() { return g_wait_limit ? g_wait_limit : kDefaultWait
 
 // Which forward kernel runs and how the keys are split.  The host knows the rows,
 // not the sequences' lengths, and goes by their average; either kernel is right for
-// any.  Up to 16 flattened rows per sequence: the 16-row kernel.  Keys are split when
+// any.  Up to 16 flattened rows per sequence: the 16-row kernel (32 sequences, 32 / 8
+// heads, 4096 keys: 4 rows 100 us against 144 with the other kernel, 16 rows 108
+// against 145; with 32 rows it would read the keys twice).  Keys are split when
 // the query rows alone give fewer CTAs than the SMs take (two of the 16-row
-// kernel's waves, one of the others), in shares of at least 128 or 512 keys.
+// kernel's waves, one of the others), in shares of at least 128 or 512 keys: one
+// token over 32768 keys 41 us split, 250 whole, over 8192 25 / 68; 64 tokens over
+// 16384 keys 33 / 259, 300 over 6000 (4 heads) 31 / 102; but over 1500 keys, where
+// the second launch costs the host what the split saves, 17.5 / 17.0.
 struct PackedFwdWs {
   bool few;
   int splits;
@@ -183,8 +188,10 @@ template <int D>
 static int launch_packed_fwd(const prism_packed_params *p, const PackedArgs &a, uint8_t *ws, cudaStream_t st) {
   const PackedFwdWs w(p);
   PackedSplit sp{w.splits, reinterpret_cast<float *>(ws + w.o), reinterpret_cast<float *>(ws + w.lse2)};
-  // Pairs of tiles from 512 keys per sequence on, single tiles below: 8192 keys 299
-  // against 313 us, 910 keys 110 against 115, 278 keys 38 against 34 us.
+  // Pairs of tiles from 512 keys per sequence on, single tiles below.  Pairs against
+  // single, 16 / 4 heads of 128, 8192 causal rows in equal sequences: of 256 keys 45.5
+  // against 43.2 us, of 512 53.3 / 52.7, of 1024 68.0 / 69.6, of 4096 140 / 162; 9
+  // sequences of 119 to 3540, 99 / 107.
   const int rc = w.few ? launch_packed_fwd_rows<D>(p, a, sp, st) : p->k_rows / p->seqs < 512 ? launch_packed_fwd_tc<D, 1>(p, a, sp, st) : launch_packed_fwd_tc<D, 2>(p, a, sp, st);
   if (rc) return rc;
   if (w.splits > 1) {
