@@ -326,6 +326,58 @@ def test_no_rows():
     P.prism_device_status()
 
 
+@pytest.mark.parametrize("heads,kv,dim", [(100, 1, 64), (128, 1, 128), (65, 1, 128), (256, 2, 64)])
+def test_a_tile_per_token(heads, kv, dim):
+    """Groups so large that a tile of 128 rows holds one token, whole or cut."""
+    gen = torch.Generator().manual_seed(heads)
+    qo = ref.offsets([5, 0, 130])
+    q, dout = (_randn(gen, qo[-1], heads, dim) for _ in range(2))
+    k, v = (_randn(gen, qo[-1], kv, dim) for _ in range(2))
+    for causal in (True, False):
+        att = PackedAttention(heads, kv, dim, causal=causal)
+        o = att.forward(q, k, v, _ints(qo))
+        grads = att.backward(dout)
+        P.prism_device_status()
+        _check(q, k, v, dout, qo, qo, causal, 0.0, None, att, o, grads, f"{heads} heads", average=True)
+
+
+def test_graph_replayed_over_other_lengths():
+    """Offsets and lengths are read on the device: a captured step, and a captured token over growing caches, serve
+    what the arrays hold when they are replayed."""
+    gen = torch.Generator().manual_seed(31)
+    q, k, v, dout = (_randn(gen, 1200, h, 128) for h in (4, 2, 2, 4))
+    lens = [[1200, 0, 0], [0, 1, 1199], [400, 500, 300], [100, 0, 900]]
+    off = _ints(ref.offsets(lens[2]))
+    cache_k, cache_v, tok = _randn(gen, 3, 900, 2, 128), _randn(gen, 3, 900, 2, 128), _randn(gen, 3, 4, 128)
+    used = _ints([1, 2, 3])
+    att, dec = PackedAttention(4, 2, 128), PackedAttention(4, 2, 128, training=False)
+    out, dq = (torch.zeros_like(q) for _ in range(2))
+    dk, dv = (torch.zeros_like(k) for _ in range(2))
+
+    def step():
+        att.forward(q, k, v, off, out=out)
+        att.backward(dout, dq, dk, dv)
+        return dec.forward(tok, cache_k, cache_v, k_used=used)
+
+    step()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        token = step()
+    lse, dec_lse = att.lse, dec.lse
+    for n, ls in enumerate(lens):
+        qo, have = ref.offsets(ls), np.array([900 - n, 300 * n, 17 + n], np.int32)
+        off.copy_(_ints(qo))
+        used.copy_(_ints(have))
+        g.replay()
+        P.prism_device_status()
+        att.lse, dec.lse = lse, dec_lse
+        _check(q, k, v, dout, qo, qo, True, 0.0, None, att, out, (dq, dk, dv), f"lengths {ls}")
+        flat = lambda t: t.reshape(2700, 2, 128)
+        _check(tok, flat(cache_k), flat(cache_v), None, np.arange(4), np.arange(4) * 900, True, 0.0, have, dec, token,
+               what=f"used {have}")
+
+
 @pytest.mark.parametrize("dim", [64, 128])
 def test_repeatable_on_streams_and_in_graphs(dim):
     """Bit-equal results run to run, on two streams at once, and from two captured graphs that are replayed
