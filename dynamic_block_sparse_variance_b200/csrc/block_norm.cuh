@@ -185,6 +185,7 @@ __global__ void __launch_bounds__(kBnWarps * 32) block_norm_fwd_kernel(const Blo
   __shared__ float red[2 * kBnWarps];
   __shared__ int abort_flag;
   int b, r0, r1;
+  after_previous();
   if (!bn_rows(a, b, r0, r1)) return;
   const int lane = threadIdx.x & 31;
   const TX *x = static_cast<const TX *>(a.x);
@@ -554,6 +555,7 @@ __global__ void __launch_bounds__(kThreads) block_norm_bwd_kernel(const BlockNor
   __shared__ __align__(16) float red[2 * (kBnMaxThreads / 32) * 8];
   __shared__ int ab;
   int b, r0, r1;
+  after_previous();
   if (!bn_rows(a, b, r0, r1)) return;
 
   const TX *xo = static_cast<const TX *>(a.x_out), *dxo = static_cast<const TX *>(a.dx_out);
@@ -800,6 +802,7 @@ __device__ __forceinline__ void put_param(void *p, int64_t i, float v, int f32) 
 
 constexpr int kBnParamWarps = 16;
 __global__ void __launch_bounds__(kBnParamWarps * 32) block_norm_params_kernel(const BnParamArgs a) {
+  after_previous();
   __shared__ float sh[kBnParamWarps][5][32];
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   const int c = blockIdx.x * 32 + lane;

@@ -57,6 +57,7 @@ template <int D>
 __global__ void __launch_bounds__(256) packed_stats_kernel(const PackedArgs a, const __nv_bfloat16 *__restrict__ o,
                                                            float *__restrict__ delta, float *__restrict__ lse2) {
   constexpr int kLanes = D / 8, kRows = 256 / kLanes;      // (row, head) pairs of a CTA and pass
+  after_previous();
   const int sub = threadIdx.x % kLanes;
   const int64_t total = (int64_t)a.qs.rows * a.heads;
   uint4 uo[2], ug[2], ur[2];

@@ -711,6 +711,7 @@ __global__ void __launch_bounds__(kPbThreads, 1)
                          const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmO,
                          const PackedArgs a, const PackedParts parts, const uint32_t limit, const int key_blocks) {
   const int block = (int)blockIdx.x;
+  after_previous();
   if (block < key_blocks) packed_keys_cta<D>(tmQ, tmK, tmV, tmO, a, parts, limit, block);
   else packed_queries_cta<D>(tmQ, tmK, tmV, tmO, a, limit, block - key_blocks, (int)gridDim.x - key_blocks);
 }
@@ -720,6 +721,7 @@ __global__ void __launch_bounds__(kPbThreads, 1)
 template <int D>
 __global__ void __launch_bounds__(256) packed_sum_kernel(const PackedArgs a, const PackedParts parts) {
   const int kvh = (int)(blockIdx.x % a.kv_heads), slot = (int)(blockIdx.x / a.kv_heads);
+  after_previous();
   int64_t piece;
   const int b = find_sequence(a.ks, slot, 1, 128, piece);
   PackedSeq s;

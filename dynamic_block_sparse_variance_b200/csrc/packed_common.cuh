@@ -15,6 +15,10 @@
 
 namespace prism {
 
+// What the kernel before this one on the stream wrote is there from here on (see
+// launch_behind); every thread calls it before its first access to global memory.
+__device__ __forceinline__ void after_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 struct Offsets {
   const int32_t *off;   // [seqs + 1], or nullptr: `even` rows each
   int seqs;

@@ -28,6 +28,7 @@ __global__ void __launch_bounds__(kPrWarps * 32) packed_fwd_rows_kernel(const Pa
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int kvh = (int)(blockIdx.x % a.kv_heads);
   const int64_t slot = blockIdx.x / a.kv_heads;
+  after_previous();
   PackedSeq::check(a, slot);
   int64_t piece;
   const int b = find_sequence(a.qs, slot, a.group, 16, piece);

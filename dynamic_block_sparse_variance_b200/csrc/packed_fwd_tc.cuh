@@ -208,6 +208,7 @@ __global__ void __launch_bounds__(64 + 128 * NG, 3 - NG)
       if (warp == 1) tc::tmem_dealloc(*tmem_slot, 256 * NG);
     }
   };
+  after_previous();
   // later tiles of a causal sequence see more keys: they start first
   const int slots = (int)(gridDim.x / a.kv_heads);
   const int kvh = (int)(blockIdx.x % a.kv_heads), slot = slots - 1 - (int)(blockIdx.x / a.kv_heads);
@@ -537,6 +538,7 @@ __global__ void __launch_bounds__(64 + 128 * NG, 3 - NG)
 template <int D>
 __global__ void __launch_bounds__(256) packed_combine_kernel(const PackedArgs a, const PackedSplit sp) {
   constexpr int kLanes = D / 4;
+  after_previous();
   const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) / kLanes;   // row * heads + head
   const int sub = threadIdx.x % kLanes;
   if (i >= (int64_t)a.qs.rows * a.heads) return;

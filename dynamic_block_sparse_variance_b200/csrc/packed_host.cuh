@@ -8,6 +8,25 @@
 
 namespace prism {
 
+// A launch that is made ready while the kernel before it on the stream runs out; the
+// kernel itself waits for that one's results (after_previous()).  About 2 us per launch
+// in a row of them: the training pass over 777 tokens 50.3 -> 47.6 us, over 6144 packed
+// tokens 251 -> 245, 61440 x 1536 block norms 145 -> 142.9.
+template <typename... P, typename... A>
+static void launch_behind(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t st, const A &...args) {
+  cudaLaunchAttribute at = {};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t c = {};
+  c.gridDim = grid;
+  c.blockDim = dim3(threads);
+  c.dynamicSmemBytes = smem;
+  c.stream = st;
+  c.attrs = &at;
+  c.numAttrs = 1;
+  cudaLaunchKernelEx(&c, kernel, args...);
+}
+
 static bool strides_ok(const int64_t s[2]) {
   return (s[0] == 0 && s[1] == 0) || (s[0] > 0 && s[1] > 0 && s[0] % 8 == 0 && s[1] % 8 == 0);
 }
@@ -160,7 +179,7 @@ static int launch_packed_fwd_rows(const prism_packed_params *p, const PackedArgs
   cudaFuncSetAttribute(packed_fwd_rows_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, kPrSmem<D>);
   const int64_t grid = slot_bound(p->q_rows, p->seqs, a.group, 16) * a.kv_heads;
   if (grid > 0x7fffffffLL) return fail(PRISM_EINVAL, "packed: too many query rows");
-  PRISM_TRACED("packed_fwd_rows_kernel", st, packed_fwd_rows_kernel<D><<<dim3((unsigned)grid, 1, sp.splits), kPrWarps * 32, kPrSmem<D>, st>>>(a, sp));
+  PRISM_TRACED("packed_fwd_rows_kernel", st, launch_behind(packed_fwd_rows_kernel<D>, dim3((unsigned)grid, 1, sp.splits), kPrWarps * 32, kPrSmem<D>, st, a, sp));
   return PRISM_OK;
 }
 
@@ -180,7 +199,7 @@ static int launch_packed_fwd_tc(const prism_packed_params *p, const PackedArgs &
   const int64_t slots = slot_bound(p->q_rows, p->seqs, a.group, 128 * NG);
   if (slots * a.kv_heads > 0x7fffffffLL) return fail(PRISM_EINVAL, "packed: too many query rows");
   const dim3 grid((unsigned)(slots * a.kv_heads), 1, sp.splits);
-  PRISM_TRACED("packed_fwd_tc_kernel", st, packed_fwd_tc_kernel<D, NG><<<grid, Cfg::kThreads, Cfg::kSmem, st>>>(tq, tk, tv, a, sp, wait_limit()));
+  PRISM_TRACED("packed_fwd_tc_kernel", st, launch_behind(packed_fwd_tc_kernel<D, NG>, grid, (int)Cfg::kThreads, Cfg::kSmem, st, tq, tk, tv, a, sp, wait_limit()));
   return PRISM_OK;
 }
 
@@ -196,7 +215,7 @@ static int launch_packed_fwd(const prism_packed_params *p, const PackedArgs &a, 
   if (rc) return rc;
   if (w.splits > 1) {
     const int64_t threads = p->q_rows * p->heads * (D / 4);
-    PRISM_TRACED("packed_combine_kernel", st, packed_combine_kernel<D><<<(unsigned)((threads + 255) / 256), 256, 0, st>>>(a, sp));
+    PRISM_TRACED("packed_combine_kernel", st, launch_behind(packed_combine_kernel<D>, dim3((unsigned)((threads + 255) / 256)), 256, 0, st, a, sp));
   }
   return PRISM_OK;
 }
@@ -217,15 +236,15 @@ static int launch_packed_bwd(const prism_packed_params *p, const PackedArgs &a, 
     return fail(PRISM_ECUDA, "cuTensorMapEncodeTiled failed");
   if (rows) {
     const int64_t threads = p->q_rows * p->heads * (D / 8);
-    PRISM_TRACED("packed_stats_kernel", st, packed_stats_kernel<D><<<(unsigned)((threads + 511) / 512), 256, 0, st>>>(a, a.o, delta, lse2));
+    PRISM_TRACED("packed_stats_kernel", st, launch_behind(packed_stats_kernel<D>, dim3((unsigned)((threads + 511) / 512)), 256, 0, st, a, (const __nv_bfloat16 *)a.o, delta, lse2));
   }
   const int64_t key_tiles = keys ? parts.tiles : 0, key_blocks = key_tiles * parts.splits;
   const int64_t blocks = key_blocks + (rows ? slot_bound(p->q_rows, p->seqs, a.group, 128) * a.kv_heads : 0);
   if (blocks > 0x7fffffffLL) return fail(PRISM_EINVAL, "packed: too many rows");
   cudaFuncSetAttribute(packed_bwd_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, kPbSmem<D>);
-  PRISM_TRACED("packed_bwd_tc_kernel", st, packed_bwd_tc_kernel<D><<<(unsigned)blocks, kPbThreads, kPbSmem<D>, st>>>(tq, tk, tv, to, a, parts, wait_limit(), (int)key_blocks));
+  PRISM_TRACED("packed_bwd_tc_kernel", st, launch_behind(packed_bwd_tc_kernel<D>, dim3((unsigned)blocks), kPbThreads, kPbSmem<D>, st, tq, tk, tv, to, a, parts, wait_limit(), (int)key_blocks));
   if (parts.splits > 1 && keys)
-    PRISM_TRACED("packed_sum_kernel", st, packed_sum_kernel<D><<<dim3((unsigned)key_tiles, D / 32), 256, 0, st>>>(a, parts));
+    PRISM_TRACED("packed_sum_kernel", st, launch_behind(packed_sum_kernel<D>, dim3((unsigned)key_tiles, D / 32), 256, 0, st, a, parts));
   return PRISM_OK;
 }
 
@@ -359,7 +378,7 @@ struct NormBwdShape {
 template <typename TX, typename TY, int V>
 static int launch_norm_fwd_v(const NormFwdShape &s, const BlockNormArgs &a, cudaStream_t st) {
   cudaFuncSetAttribute(block_norm_fwd_kernel<TX, TY, V>, cudaFuncAttributeMaxDynamicSharedMemorySize, kBnSmem);
-  PRISM_TRACED("block_norm_fwd_kernel", st, block_norm_fwd_kernel<TX, TY, V><<<(unsigned)s.slots, s.threads, s.smem, st>>>(a));
+  PRISM_TRACED("block_norm_fwd_kernel", st, launch_behind(block_norm_fwd_kernel<TX, TY, V>, dim3((unsigned)s.slots), s.threads, s.smem, st, a));
   return PRISM_OK;
 }
 template <typename TX, typename TY>
@@ -379,9 +398,9 @@ static int launch_norm_fwd(const prism_norm_params *p, BlockNormArgs &a, cudaStr
 }
 template <typename TX, typename TY, int V, int kThreads>
 static int launch_norm_bwd_v(const NormBwdShape &s, const BlockNormArgs &a, cudaStream_t st) {
-  const auto kernel = block_norm_bwd_kernel<TX, TY, V, kThreads>;
+  void (*const kernel)(const BlockNormArgs) = block_norm_bwd_kernel<TX, TY, V, kThreads>;
   cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kBnSmem);
-  PRISM_TRACED("block_norm_bwd_kernel", st, kernel<<<(unsigned)s.slots, s.threads, s.smem, st>>>(a));
+  PRISM_TRACED("block_norm_bwd_kernel", st, launch_behind(kernel, dim3((unsigned)s.slots), s.threads, s.smem, st, a));
   return PRISM_OK;
 }
 template <typename TX, typename TY>
@@ -580,7 +599,7 @@ int prism_block_norm_bwd(const prism_norm_params *p, const void *x_out, const vo
   q.per_scale = p->scale_stride != 0;
   q.per_shift = p->shift_stride != 0;
   const bool per = (dgate && q.per_gate) || (dscale && q.per_scale) || (dshift && q.per_shift);
-  PRISM_TRACED("block_norm_params_kernel", st, block_norm_params_kernel<<<dim3((unsigned)((a.C + 31) / 32), per ? 1 + p->seqs : 1), kBnParamWarps * 32, 0, st>>>(q));
+  PRISM_TRACED("block_norm_params_kernel", st, launch_behind(block_norm_params_kernel, dim3((unsigned)((a.C + 31) / 32), per ? 1 + p->seqs : 1), kBnParamWarps * 32, 0, st, q));
   return PRISM_OK;
 }
 
