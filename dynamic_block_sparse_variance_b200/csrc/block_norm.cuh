@@ -11,8 +11,8 @@
 // bytes in flight do not depend on registers.  What sets the time otherwise is
 // the reductions: with a row spread over a whole CTA (8 columns a thread) every
 // statistic is a butterfly, a barrier and a table, about 1000 cycles of
-// dependent latency, and most instructions (61440 x 1536 forward: 208 us, 145 us as
-// it is now, 5.2 TB/s, 0.79 of the measured copy rate).  So
+// dependent latency, and most instructions (61440 x 1536 forward: 208 us, 143 us as
+// it is now, 5.3 TB/s, 0.81 of the measured copy rate).  So
 //   forward   a row belongs to one warp (2 to 4 beyond 2048 channels), which
 //             keeps it in registers; warps run on their own, without barriers
 //   backward  the column sums, three per column, want to stay in registers, so

@@ -11,7 +11,9 @@ namespace prism {
 // A launch that is made ready while the kernel before it on the stream runs out; the
 // kernel itself waits for that one's results (after_previous()).  About 2 us per launch
 // in a row of them: the training pass over 777 tokens 50.3 -> 47.6 us, over 6144 packed
-// tokens 251 -> 245, 61440 x 1536 block norms 145 -> 142.9.
+// tokens 251 -> 245, 61440 x 1536 block norms 145 -> 142.9.  A go-ahead from the kernel's
+// own start (griddepcontrol.launch_dependents), so that the next one's blocks wait on the
+// SMs as they come free, was slower: those 6144 tokens 267.
 template <typename... P, typename... A>
 static void launch_behind(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t st, const A &...args) {
   cudaLaunchAttribute at = {};
