@@ -24,7 +24,7 @@ template <int D>
 __global__ void __launch_bounds__(kPrWarps * 32) packed_fwd_rows_kernel(const PackedArgs a, const PackedSplit sp) {
   constexpr int CH = D / 8, kTile = kPrKeys * D * 2;
   extern __shared__ __align__(128) uint8_t pr_smem[];
-  __shared__ float sm[kPrWarps][16], sl[kPrWarps][16];
+  __shared__ float sm[kPrWarps][16], sl[kPrWarps][16], sn[kPrWarps][16];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int kvh = (int)(blockIdx.x % a.kv_heads);
   const int64_t slot = blockIdx.x / a.kv_heads;
@@ -89,7 +89,7 @@ __global__ void __launch_bounds__(kPrWarps * 32) packed_fwd_rows_kernel(const Pa
   float acc[D / 8][4];
 #pragma unroll
   for (int t = 0; t < D / 8; ++t) acc[t][0] = acc[t][1] = acc[t][2] = acc[t][3] = 0.f;
-  float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+  float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f}, nr[2] = {0.f, 0.f};   // nr: sum of P as rounded
   const float sl2 = a.scale_log2;
   int st = 0;
   for (int t = t0 + warp; t < t1; t += kPrWarps) {
@@ -128,6 +128,7 @@ __global__ void __launch_bounds__(kPrWarps * 32) packed_fwd_rows_kernel(const Pa
       c[r] = tc::ex2(m[r] - mm[r]);
       m[r] = mx[r];
       l[r] *= c[r];
+      nr[r] *= c[r];
     }
     uint32_t p[kPrKeys / 16][4];
 #pragma unroll
@@ -136,9 +137,13 @@ __global__ void __launch_bounds__(kPrWarps * 32) packed_fwd_rows_kernel(const Pa
       const float p2 = tc::ex2(x[n][2] - mm[1]), p3 = tc::ex2(x[n][3] - mm[1]);
       l[0] += p0 + p1;
       l[1] += p2 + p3;
-      // P enters the product as bf16, as in the other forward kernel
-      p[n >> 1][(n & 1) * 2] = pack_bf16(p0, p1);
-      p[n >> 1][(n & 1) * 2 + 1] = pack_bf16(p2, p3);
+      // P enters the product as bf16, and what divides O sums it after that
+      // rounding, as in the other forward kernel
+      const uint32_t a01 = pack_bf16(p0, p1), a23 = pack_bf16(p2, p3);
+      p[n >> 1][(n & 1) * 2] = a01;
+      p[n >> 1][(n & 1) * 2 + 1] = a23;
+      nr[0] += bf16_lo(a01) + bf16_hi(a01);
+      nr[1] += bf16_lo(a23) + bf16_hi(a23);
     }
 #pragma unroll
     for (int d = 0; d < D / 8; ++d) {
@@ -162,9 +167,12 @@ __global__ void __launch_bounds__(kPrWarps * 32) packed_fwd_rows_kernel(const Pa
   for (int r = 0; r < 2; ++r) {
     l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
     l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
+    nr[r] += __shfl_xor_sync(0xffffffffu, nr[r], 1);
+    nr[r] += __shfl_xor_sync(0xffffffffu, nr[r], 2);
     if ((lane & 3) == 0) {
       sm[warp][(lane >> 2) + 8 * r] = m[r];
       sl[warp][(lane >> 2) + 8 * r] = l[r];
+      sn[warp][(lane >> 2) + 8 * r] = nr[r];
     }
   }
   __syncthreads();      // all rings are idle: they hold the four warps' O next, fp32 [warp][16][D]
@@ -185,17 +193,19 @@ __global__ void __launch_bounds__(kPrWarps * 32) packed_fwd_rows_kernel(const Pa
   constexpr int kPieces = D / 4;
   for (int i = threadIdx.x; i < rows * kPieces; i += kPrWarps * 32) {
     const int row = i / kPieces, c4 = (i % kPieces) * 4;
-    float top = sm[0][row], sum = 0.f;
+    float top = sm[0][row], sum = 0.f, nsum = 0.f;
 #pragma unroll
     for (int w = 1; w < kPrWarps; ++w) top = fmaxf(top, sm[w][row]);
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
     for (int w = 0; w < kPrWarps; ++w) {
-      if (top > -INFINITY) sum += sl[w][row] * tc::ex2(sm[w][row] - top);
+      const float f = top > -INFINITY ? tc::ex2(sm[w][row] - top) : 0.f;
+      sum += sl[w][row] * f;
+      nsum += sn[w][row] * f;
       const float4 q = *reinterpret_cast<const float4 *>(so + (w * 16 + row) * D + c4);
       o.x += q.x; o.y += q.y; o.z += q.z; o.w += q.w;
     }
-    const float inv = sum > 0.f ? 1.f / sum : 0.f;
+    const float inv = nsum > 0.f ? 1.f / nsum : 0.f;
     const float v[4] = {o.x * inv, o.y * inv, o.z * inv, o.w * inv};
     const int fr = r0 + row, tok = fr / a.group, head = kvh * a.group + fr - tok * a.group;
     const int64_t at = s.q0 + tok;

@@ -124,6 +124,9 @@ __device__ __forceinline__ void flush_rows(const uint8_t *tile, int row0, __nv_b
   __syncwarp();
 }
 
+// The two probabilities of a packed pair as they enter the product.
+__device__ __forceinline__ float2 rounded_pair(uint32_t w) { return tc::f2(bf16_lo(w), bf16_hi(w)); }
+
 struct PackedSplit {
   int splits;
   float *o;     // [split][q_rows][heads][D]
@@ -378,7 +381,7 @@ __global__ void __launch_bounds__(64 + 128 * NG, 3 - NG)
       fence_async_smem();
       warp_arrive(b_q);
     }
-    float m_run = -INFINITY, l_run = 0.f;
+    float m_run = -INFINITY, l_run = 0.f, n_run = 0.f;
     bool ok = true;
     const int steps = t1[g] - t0;
     for (int n = 0; n < steps; ++n) {
@@ -415,12 +418,13 @@ __global__ void __launch_bounds__(64 + 128 * NG, 3 - NG)
       if (grow) {
         alpha = tc::ex2(m_run - mx);
         l_run *= alpha;
+        n_run *= alpha;
         m_run = mx;
       }
       const float mm = m_run == -INFINITY ? 0.f : m_run;   // a row that has seen nothing: 2^(-inf - 0) = 0
-      float2 r2[4];
+      float2 r2[2], n2[2];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) r2[e] = tc::f2(0.f, 0.f);
+      for (int e = 0; e < 2; ++e) r2[e] = n2[e] = tc::f2(0.f, 0.f);
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
         uint32_t pk[16];
@@ -429,9 +433,13 @@ __global__ void __launch_bounds__(64 + 128 * NG, 3 - NG)
           const float2 x = tc::fma2(tc::f2u(raw[c][2 * e], raw[c][2 * e + 1]), tc::f2(sl2, sl2), tc::f2(-mm, -mm));
           const float2 p = tc::f2(tc::ex2(x.x), tc::ex2(x.y));
           // P enters the product as bf16 (V's type: both operands of one product
-          // have one type); l sums it in fp32 before that rounding
+          // have one type).  l, of which LSE is made, sums it in fp32 before that
+          // rounding; what divides O sums it after: O is then an average of the
+          // values whatever the rounding did (with l it would carry their common
+          // part times the rounding's sum, and D = rowsum(dO o O) with it)
           pk[e] = pack_bf16(p.x, p.y);
-          r2[e & 3] = tc::fma2(p, tc::f2(1.f, 1.f), r2[e & 3]);
+          r2[e & 1] = tc::fma2(p, tc::f2(1.f, 1.f), r2[e & 1]);
+          n2[e & 1] = tc::fma2(rounded_pair(pk[e]), tc::f2(1.f, 1.f), n2[e & 1]);
         }
         tc::tmem_st16(tS(g) + lane_off + 16u * c, pk);
       }
@@ -448,7 +456,8 @@ __global__ void __launch_bounds__(64 + 128 * NG, 3 - NG)
           tc::tmem_st32(tO(g) + lane_off + 32u * c, ov);
         }
       }
-      l_run += ((r2[0].x + r2[0].y) + (r2[1].x + r2[1].y)) + ((r2[2].x + r2[2].y) + (r2[3].x + r2[3].y));
+      l_run += (r2[0].x + r2[0].y) + (r2[1].x + r2[1].y);
+      n_run += (n2[0].x + n2[0].y) + (n2[1].x + n2[1].y);
       tc::tmem_st_wait();
       tc::tc_fence_before();
       if (!(a.debug_stall && n == 0)) warp_arrive(b_pfull(g));
@@ -464,7 +473,7 @@ __global__ void __launch_bounds__(64 + 128 * NG, 3 - NG)
         if (!__all_sync(0xffffffffu, tc::mbar_wait(b_q, 0, abort, limit))) ok = false;
       }
       if (ok) {
-        const float inv = l_run > 0.f ? 1.f / l_run : 0.f;
+        const float inv = n_run > 0.f ? 1.f / n_run : 0.f;
         const int head = kvh * a.group + fr - tok * a.group;
         const int64_t grow_ = s.q0 + tok;
         const auto load_o = [&](int c, uint32_t (&v)[32]) {
