@@ -23,7 +23,13 @@
 // read from shared memory (S and dP both of theirs, 64 KB per 128 x 128 x 128).
 //
 // P and dS enter their products rounded once to bf16, the type of dO, Q and K
-// (a product's operands have one type); everything else is fp32.
+// (a product's operands have one type); everything else is fp32.  A row of dS sums
+// to zero, so dQ has nothing of what the keys have in common; a row of rounded dS
+// does not, and dQ would take its sum times that common part, which in keys with a
+// bias is many times the rest (13 times: dQ off by 2% of its norm, and by 17% with
+// values like that).  The queries kind therefore sums each row of the dS that enter
+// the product and takes the sum times the keys' common part (common_key) away at the
+// end: right for any vector in its place, since the true sum is zero.
 //
 // Warps of either kind: 0 TMA producer, 1 MMA issuer and tensor-memory owner,
 // 2-9 elementwise, a row of the tile per thread (its tensor-memory lane), warps
@@ -53,9 +59,10 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatil
 
 // dS = P (dP - D) over 64 columns of dP starting at `src`, packed to bf16 at `dst`
 // in chunks of 16 columns; chunk c + 1 is loaded while chunk c is computed.
-// delta(j): D of column j (a multiple of 4) .. j + 3.
-template <typename F>
-__device__ __forceinline__ void form_ds(uint32_t src, uint32_t dst, const uint32_t (&p)[64], F delta) {
+// delta(j): D of column j (a multiple of 4) .. j + 3.  kSum: sum, the rounded dS are
+// added to it.
+template <bool kSum, typename F>
+__device__ __forceinline__ void form_ds(uint32_t src, uint32_t dst, const uint32_t (&p)[64], F delta, float2 &sum) {
   uint32_t a[16], b[16];
   tc::tmem_ld16(src, a);
   tc::tmem_ld_wait_regs(a);
@@ -73,6 +80,10 @@ __device__ __forceinline__ void form_ds(uint32_t src, uint32_t dst, const uint32
       const float2 y = tc::mul2(tc::f2u(p[j + 2], p[j + 3]), tc::sub2(tc::f2u(cur[4 * g + 2], cur[4 * g + 3]), tc::f2(d.z, d.w)));
       w[2 * g] = pack_bf16(x.x, x.y);
       w[2 * g + 1] = pack_bf16(y.x, y.y);
+      if constexpr (kSum) {
+        sum = tc::fma2(rounded_pair(w[2 * g]), tc::f2(1.f, 1.f), sum);
+        sum = tc::fma2(rounded_pair(w[2 * g + 1]), tc::f2(1.f, 1.f), sum);
+      }
     }
     if (c < 3) tc::tmem_ld_wait_regs(nxt);
     tc::tmem_st8(dst + 8u * c, w);   // dst may be src: columns below 16 (c + 1) have been read
@@ -80,9 +91,11 @@ __device__ __forceinline__ void form_ds(uint32_t src, uint32_t dst, const uint32
 }
 
 // COLS columns of an accumulator row (zeros where `zero`), times `mul`, as bf16 into row
-// `row` of a tile in shared memory, from piece ch0 on.
-template <int D, int COLS>
-__device__ __forceinline__ void put_row(uint32_t taddr, bool zero, float mul, uint8_t *tile, int row, int ch0) {
+// `row` of a tile in shared memory, from piece ch0 on.  kLess: less `sum` times the vector
+// `common` (of these columns).
+template <int D, int COLS, bool kLess = false>
+__device__ __forceinline__ void put_row(uint32_t taddr, bool zero, float mul, uint8_t *tile, int row, int ch0,
+                                        float sum = 0.f, const float *common = nullptr) {
 #pragma unroll
   for (int c = 0; c < COLS / 32; ++c) {
     uint32_t v[32];
@@ -93,8 +106,11 @@ __device__ __forceinline__ void put_row(uint32_t taddr, bool zero, float mul, ui
       uint4 w;
       uint32_t *const wp = &w.x;
 #pragma unroll
-      for (int e = 0; e < 4; ++e)
-        wp[e] = zero ? 0u : pack_bf16(__uint_as_float(v[8 * j + 2 * e]) * mul, __uint_as_float(v[8 * j + 2 * e + 1]) * mul);
+      for (int e = 0; e < 4; ++e) {
+        float2 x = tc::f2u(v[8 * j + 2 * e], v[8 * j + 2 * e + 1]);
+        if constexpr (kLess) x = tc::fma2(tc::f2(-sum, -sum), *reinterpret_cast<const float2 *>(common + 32 * c + 8 * j + 2 * e), x);
+        wp[e] = zero ? 0u : pack_bf16(x.x * mul, x.y * mul);
+      }
       *reinterpret_cast<uint4 *>(tile + Tile<D>::off(row, ch0 + 4 * c + j)) = w;
     }
   }
@@ -400,7 +416,8 @@ __device__ __forceinline__ void packed_keys_cta(const CUtensorMap &tmQ, const CU
         break;
       }
       tc::tc_fence_after();
-      form_ds(colDP, colDP, p, [&](int j) { return st[32 + j / 4]; });
+      float2 none = tc::f2(0.f, 0.f);
+      form_ds<false>(colDP, colDP, p, [&](int j) { return st[32 + j / 4]; }, none);
       tc::tmem_st_wait();
       tc::tc_fence_before();
       warp_arrive(b_ds);
@@ -439,6 +456,44 @@ __device__ __forceinline__ void packed_keys_cta(const CUtensorMap &tmQ, const CU
     tc::tc_fence_after();
     tc::tmem_dealloc(tmem, 512);
   }
+}
+
+// A barrier of the eight elementwise warps.
+__device__ __forceinline__ void elementwise_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
+
+// What the first n keys of a sequence (kv head's keys at `k`) have in common, into the first
+// D floats of `room`, 2 KB of shared memory, by the elementwise warps (t: 0 .. 255): the
+// mean of 64 keys spread evenly over them, in the columns where it is beyond four of its
+// standard errors, and zero in the others, whose mean is chance and would only add to dQ's
+// error.  The partial sums pass through bf16: any vector will do, as long as every row of
+// the tile takes the same.
+template <int D>
+__device__ __forceinline__ void common_key(const __nv_bfloat16 *k, int64_t row_stride, int n, uint8_t *room, int t) {
+  constexpr int kPairs = D / 2, kParts = 256 / kPairs, kKeys = 64;
+  uint32_t *const part = reinterpret_cast<uint32_t *>(room);      // [sums | squares][kParts][kPairs]
+  const int col = t % kPairs, first = t / kPairs;
+  float2 m = tc::f2(0.f, 0.f), q = tc::f2(0.f, 0.f);
+#pragma unroll
+  for (int i = 0; i < kKeys / kParts; ++i) {
+    const int64_t key = (int64_t)(2 * (first + i * kParts) + 1) * n / (2 * kKeys);      // < n
+    const float2 x = rounded_pair(*reinterpret_cast<const uint32_t *>(k + key * row_stride + 2 * col));
+    m = tc::fma2(x, tc::f2(1.f / kKeys, 1.f / kKeys), m);
+    q = tc::fma2(tc::mul2(x, tc::f2(1.f / kKeys, 1.f / kKeys)), x, q);
+  }
+  part[t] = pack_bf16(m.x, m.y);
+  part[256 + t] = pack_bf16(q.x, q.y);
+  elementwise_sync();
+  m = q = tc::f2(0.f, 0.f);
+  if (t < kPairs)
+    for (int i = 0; i < kParts; ++i) {
+      m = tc::fma2(rounded_pair(part[i * kPairs + t]), tc::f2(1.f, 1.f), m);
+      q = tc::fma2(rounded_pair(part[256 + i * kPairs + t]), tc::f2(1.f, 1.f), q);
+    }
+  elementwise_sync();
+  const float least = 16.f / (float)min(n, kKeys);      // mean^2 > 16 variance / keys
+  if (t < kPairs)
+    reinterpret_cast<float2 *>(room)[t] = tc::f2(m.x * m.x > least * (q.x - m.x * m.x) ? m.x : 0.f,
+                                                 m.y * m.y > least * (q.y - m.y * m.y) ? m.y : 0.f);
 }
 
 // The kind that keeps dQ, `block` of `blocks`.
@@ -482,7 +537,7 @@ __device__ __forceinline__ void packed_queries_cta(const CUtensorMap &tmQ, const
   if (piece < 0 || piece * 128 >= nrows) return;
   const int r0 = (int)(piece * 128);
   const int rows = (int)min((int64_t)128, nrows - r0);
-  const int nsteps = (s.visible(a, (r0 + rows - 1) / a.group) + 127) >> 7;
+  const int keys = s.visible(a, (r0 + rows - 1) / a.group), nsteps = (keys + 127) >> 7;
   const bool q_copy = 128 % a.group == 0;
 
   if (threadIdx.x == 0) {
@@ -645,6 +700,11 @@ __device__ __forceinline__ void packed_queries_cta(const CUtensorMap &tmQ, const
       fence_async_smem();
       warp_arrive(b_qo);
     }
+    // the first D floats of `room`: the common part of the keys; from 1 KB on, at the end: [half][row] sums of dS
+    uint8_t *const room = sgen + 7 * T::kBytes;
+    if (nsteps > 0)
+      common_key<D>(a.k + (int64_t)s.k0 * a.sk[0] + (int64_t)kvh * a.sk[1], a.sk[0], keys, room, (int)threadIdx.x - 64);
+    float2 ds_sum = tc::f2(0.f, 0.f);
     for (int n = 0; n < nsteps; ++n) {
       if (!warp_wait(b_s(n & 1), (uint32_t)(n >> 1) & 1u, abort, limit)) {
         ok = false;
@@ -677,19 +737,24 @@ __device__ __forceinline__ void packed_queries_cta(const CUtensorMap &tmQ, const
         break;
       }
       tc::tc_fence_after();
-      form_ds(tDP + lane_off + 64u * half, colS, p, [&](int) { return d4; });
+      form_ds<true>(tDP + lane_off + 64u * half, colS, p, [&](int) { return d4; }, ds_sum);
       tc::tmem_st_wait();
       tc::tc_fence_before();
       if (!(a.debug_stall && n == 0)) warp_arrive(b_ds);
     }
+    float *const sums = reinterpret_cast<float *>(room + 1024);
+    sums[128 * half + row] = ds_sum.x + ds_sum.y;
+    elementwise_sync();      // (after a wait that ran out too)
     if (__all_sync(0xffffffffu, ok && !*abort)) {
       if (nsteps > 0) ok = warp_wait(b_drain, 0, abort, limit);
       if (ok) {
         tc::tc_fence_after();
         constexpr int kCols = D / 2;
+        const float sum = sums[row] + sums[128 + row];
         uint8_t *const tile = sgen + (sQ - sbase);      // every product that reads Q is done
         const int ch0 = half * (kCols / 8);
-        put_row<D, kCols>(tdQ + lane_off + (uint32_t)(half * kCols), nsteps == 0, a.scale, tile, row, ch0);
+        put_row<D, kCols, true>(tdQ + lane_off + (uint32_t)(half * kCols), nsteps == 0, a.scale, tile, row, ch0, sum,
+                                reinterpret_cast<const float *>(room) + half * kCols);
         flush_rows<D, kCols>(tile, 32 * q, have ? a.dq + (int64_t)(s.q0 + tok) * a.sdq[0] + (int64_t)head * a.sdq[1] + half * kCols : nullptr, ch0);
       }
     }
