@@ -24,6 +24,7 @@
 #pragma once
 
 #include "packed_common.cuh"
+#include "packed_runs.cuh"
 #include "tc_common.cuh"
 
 namespace prism {
@@ -146,10 +147,7 @@ __device__ __forceinline__ bool bn_rows(const BlockNormArgs &a, int &b, int &r0,
   b = find_sequence(a.seq, blockIdx.x, 1, a.unit, piece);
   int begin, len;
   if (!sequence_rows(a.seq, b, begin, len)) return false;
-  if (piece < 0 || piece * a.unit >= len) return false;
-  r0 = begin + (int)piece * a.unit;
-  r1 = min(begin + len, r0 + a.unit);
-  return true;
+  return run_rows(begin, len, piece, a.unit, r0, r1);
 }
 
 // ---- forward -------------------------------------------------------------------
@@ -820,12 +818,12 @@ __global__ void __launch_bounds__(kBnParamWarps * 32) block_norm_params_kernel(c
     const float ws = all && a.dweight && a.scale ? 1.f + param_at(a.scale, b * a.sscale + c, a.param_f32) : 1.f;
     const float wg = all && a.dpost_weight && a.gate ? param_at(a.gate, b * a.sgate + c, a.param_f32) : 1.f;
     const float *p = a.part + ((int64_t)begin / a.unit + b) * a.groups * 3 * a.C + c;
-    const int n = (len + a.unit - 1) / a.unit * a.groups;
+    const int64_t n = (int64_t)run_count(len, a.unit) * a.groups;
     const bool k0 = a.need & 1, k1 = a.need & 2, k2 = a.need & 4;
     float t[3] = {0.f, 0.f, 0.f};
 #pragma unroll 4
-    for (int i = w % each; i < n; i += each) {
-      const float *q = p + (int64_t)i * 3 * a.C;
+    for (int64_t i = w % each; i < n; i += each) {
+      const float *q = p + i * 3 * a.C;
       if (k0) t[0] += q[0];
       if (k1) t[1] += q[a.C];
       if (k2) t[2] += q[2 * (int64_t)a.C];
