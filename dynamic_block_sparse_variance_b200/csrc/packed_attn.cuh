@@ -51,7 +51,7 @@ struct PackedSeq {
 
 // Per query row and head (8 or 16 lanes, 8 columns each; two rows at a time, so that
 // six 16-byte loads are in flight): D = rowsum(dO o (O + residual)) and LSE log2e; a
-// row that sees nothing gets +inf, so that its probabilities 2^(x - inf) are zero.
+// row that sees nothing (LSE -inf) gets +inf, so that its probabilities 2^(x - inf) are zero.
 // Written in flattened order.
 template <int D>
 __global__ void __launch_bounds__(256) packed_stats_kernel(const PackedArgs a, const __nv_bfloat16 *__restrict__ o,
@@ -95,7 +95,7 @@ __global__ void __launch_bounds__(256) packed_stats_kernel(const PackedArgs a, c
       const int kvh = h[p] / a.group;
       const int64_t at = ((int64_t)kvh * a.qs.rows + row[p]) * a.group + h[p] - kvh * a.group;
       delta[at] = s;
-      lse2[at] = isfinite(L[p]) ? L[p] * kLog2e : INFINITY;
+      lse2[at] = L[p] == -INFINITY ? INFINITY : L[p] * kLog2e;
     }
   }
 }

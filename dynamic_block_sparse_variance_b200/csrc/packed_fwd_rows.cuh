@@ -199,17 +199,17 @@ __global__ void __launch_bounds__(kPrWarps * 32) packed_fwd_rows_kernel(const Pa
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
     for (int w = 0; w < kPrWarps; ++w) {
-      const float f = top > -INFINITY ? tc::ex2(sm[w][row] - top) : 0.f;
+      const float f = top > -INFINITY ? tc::ex2(sm[w][row] - top) : 1.f;      // 1: the sums are 0 or NaN
       sum += sl[w][row] * f;
       nsum += sn[w][row] * f;
       const float4 q = *reinterpret_cast<const float4 *>(so + (w * 16 + row) * D + c4);
       o.x += q.x; o.y += q.y; o.z += q.z; o.w += q.w;
     }
-    const float inv = nsum > 0.f ? 1.f / nsum : 0.f;
+    const float inv = nsum == 0.f ? 0.f : 1.f / nsum;      // 0: saw no key; NaN stays NaN
     const float v[4] = {o.x * inv, o.y * inv, o.z * inv, o.w * inv};
     const int fr = r0 + row, tok = fr / a.group, head = kvh * a.group + fr - tok * a.group;
     const int64_t at = s.q0 + tok;
-    const float l2 = sum > 0.f ? top + log2f(sum) : -INFINITY;
+    const float l2 = sum == 0.f ? -INFINITY : top + log2f(sum);
     if (sp.splits > 1) {
       *reinterpret_cast<float4 *>(sp.o + (((int64_t)blockIdx.z * a.qs.rows + at) * a.heads + head) * D + c4) =
           make_float4(v[0], v[1], v[2], v[3]);

@@ -473,7 +473,7 @@ __global__ void __launch_bounds__(64 + 128 * NG, 3 - NG)
         if (!__all_sync(0xffffffffu, tc::mbar_wait(b_q, 0, abort, limit))) ok = false;
       }
       if (ok) {
-        const float inv = n_run > 0.f ? 1.f / n_run : 0.f;
+        const float inv = n_run == 0.f ? 0.f : 1.f / n_run;      // 0: saw no key; NaN stays NaN
         const int head = kvh * a.group + fr - tok * a.group;
         const int64_t grow_ = s.q0 + tok;
         const auto load_o = [&](int c, uint32_t (&v)[32]) {
@@ -527,7 +527,7 @@ __global__ void __launch_bounds__(64 + 128 * NG, 3 - NG)
           }
         }
         if (have) {
-          const float l2 = l_run > 0.f ? m_run + log2f(l_run) : -INFINITY;
+          const float l2 = l_run == 0.f ? -INFINITY : m_run + log2f(l_run);
           if (sp.splits > 1) sp.lse2[((int64_t)blockIdx.z * a.heads + head) * a.qs.rows + grow_] = l2;
           else a.lse[(int64_t)head * a.qs.rows + grow_] = l2 * kLn2;
         }
@@ -543,7 +543,8 @@ __global__ void __launch_bounds__(64 + 128 * NG, 3 - NG)
 }
 
 // Joins the shares of split keys: O = sum_s 2^(L_s - L) O_s with L = log2 sum_s 2^(L_s).
-// D / 4 threads per (row, head), shares summed in order.
+// D / 4 threads per (row, head), shares summed in order.  A share that saw no key of the row
+// has L_s = -inf and O_s = 0, one with a NaN has both NaN, and so has the row.
 template <int D>
 __global__ void __launch_bounds__(256) packed_combine_kernel(const PackedArgs a, const PackedSplit sp) {
   constexpr int kLanes = D / 4;
@@ -561,25 +562,24 @@ __global__ void __launch_bounds__(256) packed_combine_kernel(const PackedArgs a,
   float m = -INFINITY;
 #pragma unroll 4
   for (int s = 0; s < sp.splits; ++s) m = fmaxf(m, L[s * ls]);
+  if (m == -INFINITY) m = 0.f;                    // no share saw a number: weights of 0 or NaN
   float l = 0.f;
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (m > -INFINITY) {
 #pragma unroll 4
-    for (int s = 0; s < sp.splits; ++s) {
-      const float w = exp2f(L[s * ls] - m);       // 0 for a share without keys, whose O is 0
-      const float4 p = *reinterpret_cast<const float4 *>(sp.o + (s * (int64_t)a.qs.rows * a.heads + i) * D + sub * 4);
-      l += w;
-      o.x = fmaf(w, p.x, o.x); o.y = fmaf(w, p.y, o.y); o.z = fmaf(w, p.z, o.z); o.w = fmaf(w, p.w, o.w);
-    }
+  for (int s = 0; s < sp.splits; ++s) {
+    const float w = exp2f(L[s * ls] - m);
+    const float4 p = *reinterpret_cast<const float4 *>(sp.o + (s * (int64_t)a.qs.rows * a.heads + i) * D + sub * 4);
+    l += w;
+    o.x = fmaf(w, p.x, o.x); o.y = fmaf(w, p.y, o.y); o.z = fmaf(w, p.z, o.z); o.w = fmaf(w, p.w, o.w);
   }
-  const float inv = l > 0.f ? 1.f / l : 0.f;
+  const float inv = l == 0.f ? 0.f : 1.f / l;
   const float x[4] = {o.x * inv, o.y * inv, o.z * inv, o.w * inv};
   const uint2 u = make_uint2(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]));
   *reinterpret_cast<uint2 *>(a.o + row * a.so[0] + h * a.so[1] + sub * 4) = u;
   if (a.o_res)
     *reinterpret_cast<uint2 *>(a.o_res + i * D + sub * 4) =
         make_uint2(pack_bf16(x[0] - bf16_lo(u.x), x[1] - bf16_hi(u.x)), pack_bf16(x[2] - bf16_lo(u.y), x[3] - bf16_hi(u.y)));
-  if (sub == 0) a.lse[(int64_t)h * a.qs.rows + row] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+  if (sub == 0) a.lse[(int64_t)h * a.qs.rows + row] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
 }
 
 }  // namespace prism
