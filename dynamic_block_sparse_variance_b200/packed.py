@@ -233,6 +233,21 @@ def _norm_rows(shape, stride, channels, name):
     return rows
 
 
+def _on(out, kept):
+    """Whether an output takes the place of a tensor."""
+    return out is not None and kept is not None and out.data_ptr() == kept.data_ptr() and out.numel() > 0
+
+
+def _keep(x, y, x_out, h):
+    """Refuses the in-place forms that overwrite what the backward of a training forward starts from: y, and x
+    where there is no y."""
+    if y is None:
+        _need(not _on(h, x), "h must not take the place of x, which backward() needs where there is no y")
+    else:
+        _need(not _on(h, y), "h must not take the place of y, which backward() needs")
+        _need(not _on(x_out, y), "x_out must not take the place of y, which backward() needs")
+
+
 class _NormPlan:
     __slots__ = ("p", "ws", "branch")
 
@@ -257,7 +272,8 @@ class BlockNorm:
     ``offsets`` saying which rows are whose; all of these have one type, bf16 or f32. Every parameter may be
     left out. With ``training`` forward() keeps what backward() needs: y, x_out and the parameters (not copies; leave
     them unchanged until then). Outputs may take the place of inputs of the same type and strides: x_out that of x, dx
-    that of dx_out, dy that of dh and, without training, h that of y. Rows outside every sequence are left as they were. Calls run on the device of x and its current stream.
+    that of dx_out, dy that of dh and, without training, h that of y or x and x_out that of y. A backward() whose dx or
+    dy takes the place of what it starts from is the last one of its forward(). Rows outside every sequence are left as they were. Calls run on the device of x and its current stream.
     """
 
     def __init__(self, channels, *, post="none", pre="rms", eps=1e-6, alpha=1.0, training=True):
@@ -328,10 +344,9 @@ class BlockNorm:
         params = (post_weight, gate, weight, scale, shift)
         _same_device(at, y, x_out, h, y_norms, *params)
         n_off = _index(offsets, at, "offsets")
-        if y is None:
-            _need(x_out is None, "x_out belongs to a y")
-        elif self.training and h is not None:
-            _need(h.data_ptr() != y.data_ptr() or not h.numel(), "h must not take the place of y, which backward() needs")
+        _need(y is not None or x_out is None, "x_out belongs to a y")
+        if self.training:
+            _keep(x, y, x_out, h)
         layouts = (_layout(x), _layout(y), _layout(x_out), _layout(h), h_dtype, n_off,
                    (_layout(post_weight), _layout(gate), _layout(weight), _layout(scale), _layout(shift)))
         key = (self.channels, self.post, self.pre, self.eps, self.alpha, layouts)
@@ -385,4 +400,6 @@ class BlockNorm:
         ws = kept.new_empty(plan.ws, dtype=torch.uint8)
         here = _used_here(at, stream, (kept, y, offsets, *params))
         P.prism_block_norm_bwd(p, kept, y, offsets, post_weight, gate, weight, scale, dh, dx_out, dx, dy, *grads, ws, here)
+        if _on(dx, kept) or _on(dx, y) or _on(dy, kept) or _on(dy, y):
+            self._saved = None
         return {"dx": dx, "dy": dy, **{"d" + n: g for n, g in zip(_PARAMS, grads)}}

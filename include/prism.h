@@ -434,10 +434,11 @@ typedef struct {
  *   y_norms   out, nullable: [rows] float ||y_n||_2, the indicator's audio
  *             input when y is the audio-to-video cross-attention's output
  *             (Method §1; what prism_audio_norms computes in a pass of its own)
- * An output may take the place of an input of its type and row stride (x_out that
- * of x, h that of y; in the backward dx that of dx_out, dy that of dh): a row is
- * read before it is written.  Any other overlap is the caller's mistake; where it
- * shows in the addresses alone the call is refused.
+ * An output may take the place of any input of its type and row stride: a row is
+ * read before it is written (x_out in place of x, h of y, dx of dx_out, dy of dh).
+ * What the backward starts from, x_out and y (without y: x), is the caller's to keep
+ * until then.  Any other overlap is the caller's mistake; where it shows in the
+ * addresses alone (another type or row stride, two outputs) the call is refused.
  */
 int prism_block_norm_fwd(const prism_norm_params *p, const void *x, const void *y, const int32_t *off,
                          const void *post_weight, const void *gate, const void *weight, const void *scale,
