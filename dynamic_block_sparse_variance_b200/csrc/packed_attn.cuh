@@ -54,8 +54,8 @@ struct PackedSeq {
 // row that sees nothing (LSE -inf) gets +inf, so that its probabilities 2^(x - inf) are zero.
 // Written in flattened order.
 template <int D>
-__global__ void __launch_bounds__(256) packed_stats_kernel(const PackedArgs a, const __nv_bfloat16 *__restrict__ o,
-                                                           float *__restrict__ delta, float *__restrict__ lse2) {
+__global__ void __launch_bounds__(256) packed_stats_kernel(const PackedArgs a, const __nv_bfloat16 *o, float *delta,
+                                                           float *lse2) {
   constexpr int kLanes = D / 8, kRows = 256 / kLanes;      // (row, head) pairs of a CTA and pass
   after_previous();
   const int sub = threadIdx.x % kLanes;
@@ -71,9 +71,9 @@ __global__ void __launch_bounds__(256) packed_stats_kernel(const PackedArgs a, c
     h[p] = (int)(i - row[p] * a.heads);
     uo[p] = ug[p] = ur[p] = make_uint4(0u, 0u, 0u, 0u);
     if (i < total) {
-      uo[p] = __ldg(reinterpret_cast<const uint4 *>(o + row[p] * a.so[0] + h[p] * a.so[1] + sub * 8));
-      ug[p] = __ldg(reinterpret_cast<const uint4 *>(a.dout + row[p] * a.sdo[0] + h[p] * a.sdo[1] + sub * 8));
-      if (a.o_res) ur[p] = __ldg(reinterpret_cast<const uint4 *>(a.o_res + i * D + sub * 8));
+      uo[p] = *reinterpret_cast<const uint4 *>(o + row[p] * a.so[0] + h[p] * a.so[1] + sub * 8);
+      ug[p] = *reinterpret_cast<const uint4 *>(a.dout + row[p] * a.sdo[0] + h[p] * a.sdo[1] + sub * 8);
+      if (a.o_res) ur[p] = *reinterpret_cast<const uint4 *>(a.o_res + i * D + sub * 8);
       L[p] = a.lse[(int64_t)h[p] * a.qs.rows + row[p]];
     } else {
       row[p] = -1;

@@ -16,7 +16,9 @@
 namespace prism {
 
 // What the kernel before this one on the stream wrote is there from here on (see
-// launch_behind); every thread calls it before its first access to global memory.
+// launch_behind); every thread calls it before its first access to global memory.  That
+// kernel may still write while this one is resident, so no load here is a non-coherent
+// one (__ldg, __restrict__), which promises that nobody writes during the kernel's life.
 __device__ __forceinline__ void after_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 struct Offsets {
