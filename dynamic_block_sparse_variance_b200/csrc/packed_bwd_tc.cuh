@@ -189,6 +189,7 @@ __device__ __forceinline__ void packed_keys_cta(const CUtensorMap &tmQ, const CU
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int share = block % parts.splits, kvh = block / parts.splits % a.kv_heads, slot = block / parts.splits / a.kv_heads;
+  if (a.qs.rows == 0) PackedSeq::check(a, slot);      // there is no other kind to look
   int64_t piece;
   const int b = find_sequence(a.ks, slot, 1, 128, piece);
   PackedSeq s;
