@@ -147,7 +147,11 @@ __device__ __forceinline__ bool bn_rows(const BlockNormArgs &a, int &b, int &r0,
   b = find_sequence(a.seq, blockIdx.x, 1, a.unit, piece);
   int begin, len;
   if (!sequence_rows(a.seq, b, begin, len)) return false;
-  return run_rows(begin, len, piece, a.unit, r0, r1);
+  if (!run_rows(begin, len, piece, a.unit, r0, r1)) return false;
+  // The two as plain numbers: where the compiler sees how r1 follows from r0, it orders the
+  // backward's loop otherwise (30011 x 2048: 219 us against 203).
+  asm volatile("" : "+r"(r0), "+r"(r1));
+  return true;
 }
 
 // ---- forward -------------------------------------------------------------------
