@@ -29,7 +29,10 @@
 // bias is many times the rest (13 times: dQ off by 2% of its norm, and by 17% with
 // values like that).  The queries kind therefore sums each row of the dS that enter
 // the product and takes the sum times the keys' common part (common_key) away at the
-// end: right for any vector in its place, since the true sum is zero.
+// end: right for any vector in its place, since the true sum is zero.  It is not where
+// o and lse belong to a softmax over more keys than this call's (shares of the keys
+// joined by their LSE): such a row is known by its P, which do not sum to one, and
+// keeps its sum.
 //
 // Warps of either kind: 0 TMA producer, 1 MMA issuer and tensor-memory owner,
 // 2-9 elementwise, a row of the tile per thread (its tensor-memory lane), warps
@@ -701,11 +704,12 @@ __device__ __forceinline__ void packed_queries_cta(const CUtensorMap &tmQ, const
       fence_async_smem();
       warp_arrive(b_qo);
     }
-    // the first D floats of `room`: the common part of the keys; from 1 KB on, at the end: [half][row] sums of dS
+    // `room`: D floats, the common part of the keys; at the end, from 512 bytes on, the rows' sums of dS that
+    // count, and from 1 KB on the sums of dS and of P over the second half of the columns
     uint8_t *const room = sgen + 7 * T::kBytes;
     if (nsteps > 0)
       common_key<D>(a.k + (int64_t)s.k0 * a.sk[0] + (int64_t)kvh * a.sk[1], a.sk[0], keys, room, (int)threadIdx.x - 64);
-    float2 ds_sum = tc::f2(0.f, 0.f);
+    float2 ds_sum = tc::f2(0.f, 0.f), p_sum = ds_sum;
     for (int n = 0; n < nsteps; ++n) {
       if (!warp_wait(b_s(n & 1), (uint32_t)(n >> 1) & 1u, abort, limit)) {
         ok = false;
@@ -732,6 +736,7 @@ __device__ __forceinline__ void packed_queries_cta(const CUtensorMap &tmQ, const
         }
         p[j] = __float_as_uint(tc::ex2(x.x));
         p[j + 1] = __float_as_uint(tc::ex2(x.y));
+        p_sum = tc::fma2(tc::f2u(p[j], p[j + 1]), tc::f2(1.f, 1.f), p_sum);
       }
       if (!warp_wait(b_dp, (uint32_t)n & 1u, abort, limit)) {
         ok = false;
@@ -743,15 +748,22 @@ __device__ __forceinline__ void packed_queries_cta(const CUtensorMap &tmQ, const
       tc::tc_fence_before();
       if (!(a.debug_stall && n == 0)) warp_arrive(b_ds);
     }
-    float *const sums = reinterpret_cast<float *>(room + 1024);
-    sums[128 * half + row] = ds_sum.x + ds_sum.y;
+    float *const counts = reinterpret_cast<float *>(room + 512);
+    float2 *const second = reinterpret_cast<float2 *>(room + 1024);
+    if (half) second[row] = make_float2(ds_sum.x + ds_sum.y, p_sum.x + p_sum.y);
     elementwise_sync();      // (after a wait that ran out too)
+    if (!half) {
+      // (the fp32 LSE leaves P's sum off by some 2^-22 of its size)
+      const float whole = p_sum.x + p_sum.y + second[row].y;
+      counts[row] = fabsf(whole - 1.f) <= fmaf(fabsf(nl), 0x1p-20f, 0x1p-12f) ? ds_sum.x + ds_sum.y + second[row].x : 0.f;
+    }
+    elementwise_sync();
     if (__all_sync(0xffffffffu, ok && !*abort)) {
       if (nsteps > 0) ok = warp_wait(b_drain, 0, abort, limit);
       if (ok) {
         tc::tc_fence_after();
         constexpr int kCols = D / 2;
-        const float sum = sums[row] + sums[128 + row];
+        const float sum = counts[row];
         uint8_t *const tile = sgen + (sQ - sbase);      // every product that reads Q is done
         const int ch0 = half * (kCols / 8);
         put_row<D, kCols, true>(tdQ + lane_off + (uint32_t)(half * kCols), nsteps == 0, a.scale, tile, row, ch0, sum,

@@ -384,7 +384,9 @@ int prism_packed_attn_fwd(const prism_packed_params *p, const void *q, const voi
  * Backward of prism_packed_attn_fwd: dq, dk, dv (bf16) from dout (bf16), o, lse
  * and, nullable, o_res.  dk and dv sum over the query heads of a group; key
  * rows that no query sees, and rows behind k_used, get zero.  Results do
- * not change from run to run.
+ * not change from run to run.  o and lse may belong to a softmax over more keys
+ * than the call's (shares of the keys joined by their LSE): the gradients are then
+ * the call's part.
  */
 int prism_packed_attn_bwd(const prism_packed_params *p, const void *q, const void *k, const void *v,
                           const void *o, const void *o_res, const void *dout, const float *lse,
