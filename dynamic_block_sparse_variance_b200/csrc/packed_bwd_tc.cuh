@@ -15,9 +15,9 @@
 // saves two products but writes 64 KB of reductions per tile pair and gives dQ
 // whose last bits change from run to run.
 //
-// Measured (8192 tokens, 8 heads of 128, all pairs, bursts): 854 us, 805 TFLOP/s of
-// the algorithm's 5 products, 1127 of the 7, 0.68 of the bf16 rate measured with a
-// library product; 164 us at 7 packed causal sequences of 6144 tokens in all, 16 / 4
+// Measured (8192 tokens, 8 heads of 128, all pairs, bursts): 882 us, 779 TFLOP/s of
+// the algorithm's 5 products, 1091 of the 7, 0.66 of the bf16 rate measured with a
+// library product; 172 us at 7 packed causal sequences of 6144 tokens in all, 16 / 4
 // heads.  What bounds it is a tile's chain again (S, P, its product, dP, dS, its
 // product, in all 512 columns of tensor memory), and the operands that the products
 // read from shared memory (S and dP both of theirs, 64 KB per 128 x 128 x 128).
@@ -32,7 +32,7 @@
 // end: right for any vector in its place, since the true sum is zero.  It is not where
 // o and lse belong to a softmax over more keys than this call's (shares of the keys
 // joined by their LSE): such a row is known by its P, which do not sum to one, and
-// keeps its sum.
+// keeps its sum.  (The sums cost the two cases above 25 and 8 us.)
 //
 // Warps of either kind: 0 TMA producer, 1 MMA issuer and tensor-memory owner,
 // 2-9 elementwise, a row of the tile per thread (its tensor-memory lane), warps

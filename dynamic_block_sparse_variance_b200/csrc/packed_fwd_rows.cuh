@@ -1,15 +1,15 @@
 // Dense attention forward for few query rows per sequence (a token over a cache):
 // 16 flattened rows (tokens x heads of the group) of one kv head per CTA, on the
-// warp-level m16n8k16 MMA.  Bound by reading K and V once: 32 flops a byte and
-// row at most, so the tensor rate does not matter, the bytes in flight do.
+// warp-level m16n8k16 MMA.  Bound by reading K and V once: one flop a byte and row,
+// 16 with all rows in use, so the tensor rate does not matter, the bytes in flight do.
 //
 // The keys are split over blockIdx.z and, in a CTA, over its four warps, which
 // take 32 keys in turn and never wait for one another: each fills a ring of its
 // own with cp.async (3 stages of 16 KB, 192 KB of loads in flight per SM for
 // head_dim 128), keeps its own running maximum, sum and O, and the four are joined
 // at the end.  Rows past the keys in use are not read: zeros take their place.
-// Measured (48 sequences of up to 8192 cached keys, 32 / 8 heads of 128): 172 us,
-// 6.2 TB/s, 0.95 of the measured copy rate.
+// Measured (48 sequences of up to 8192 cached keys, 32 / 8 heads of 128): 174
+// to 181 us by board, 6.0 TB/s, 0.90 to 0.94 of the measured copy rate.
 #pragma once
 
 #include "packed_fwd_tc.cuh"

@@ -17,8 +17,8 @@
 // 128 x 128 tiles the products take 2048 and the special-function unit's
 // exponentials 2048, and with S, P and O of two tiles in all 512 columns of tensor
 // memory the next S of a tile waits for its P V.  Measured (8 heads of 128, 16384
-// causal rows, bursts): 472 us, 1165 TFLOP/s, 0.71 of the bf16 rate measured with a
-// library product; under the power cap of a long run 556 us.  Slower, each against
+// causal rows, bursts): 484 us, 1136 TFLOP/s, 0.69 of the bf16 rate measured with a
+// library product; under the power cap of a long run 560 us.  Slower, each against
 // the form of its time: eight softmax warps per tile (527 against 512 us), three of
 // eight exponentials as polynomials on the FMA pipe (598 against 512: the products
 // themselves then run at 70% of their rate), 208 registers for the softmax warps,

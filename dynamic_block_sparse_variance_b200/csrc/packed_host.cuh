@@ -10,8 +10,9 @@ namespace prism {
 
 // A launch that is made ready while the kernel before it on the stream runs out; the
 // kernel itself waits for that one's results (after_previous()).  About 2 us per launch
-// in a row of them: the training pass over 777 tokens 50.3 -> 47.6 us, over 6144 packed
-// tokens 251 -> 245, 61440 x 1536 block norms 145 -> 142.9.  A go-ahead from the kernel's
+// in a row of them, both sides on one machine: the training pass over 777 tokens 50.3 ->
+// 47.6 us (on one with a faster host 46 -> 41), over 6144 packed tokens 251 -> 245,
+// 61440 x 1536 block norms 145 -> 142.9.  A go-ahead from the kernel's
 // own start (griddepcontrol.launch_dependents), so that the next one's blocks wait on the
 // SMs as they come free, was slower: those 6144 tokens 267.
 template <typename... P, typename... A>
@@ -322,11 +323,6 @@ static int norm_args(const prism_norm_params *p, const int32_t *off, const void 
 // parameters leave, and about as many runs of rows as there are SMs.
 constexpr int kBnSmem = 216 * 1024;
 static int type_bytes(int t) { return t == PRISM_F32 ? 4 : 2; }
-static int norm_unit(const prism_norm_params *p, int least) {
-  const int64_t wave = std::max<int64_t>(1, 148 - p->seqs);      // a sequence's last run may be short
-  const int64_t u = (p->rows + wave - 1) / wave;
-  return (int)std::max<int64_t>(least, u);
-}
 // Forward: a row in the registers of one warp up to 2048 channels (8 vectors of
 // 8 columns a thread), of 2 to 4 warps beyond.
 struct NormFwdShape {
@@ -340,7 +336,7 @@ struct NormFwdShape {
     V = vecs <= 1 ? 1 : vecs <= 2 ? 2 : vecs <= 4 ? 4 : 8;
     const int row = C * (type_bytes(p->stream_dtype) + (with_y ? type_bytes(p->branch_dtype) : 0));
     groups = std::max(1, std::min(kBnWarps / wpr, (kBnSmem - 12 * C) / row));
-    unit = norm_unit(p, 1);
+    unit = (int)run_length(p->rows, p->seqs, 148, 1);
     groups = std::min(groups, unit);
     stages = std::max(1, std::min({kBnMaxStages, (kBnSmem - 12 * C) / (groups * row), (unit + groups - 1) / groups}));
     smem = (size_t)12 * C + (size_t)groups * stages * row;
@@ -369,8 +365,7 @@ struct NormBwdShape {
     const int ctas = std::max(1, std::min(16 / (wpr * groups), 200 * 1024 / (2 * stage + fixed + 2048)));
     stages = std::max(1, std::min(kBnMaxStages, (200 * 1024 / ctas - fixed - 2048) / stage));
     smem = (size_t)stages * stage + fixed;
-    const int64_t wave = std::max<int64_t>(1, (int64_t)148 * ctas - p->seqs);
-    unit = (int)std::max<int64_t>(2 * groups, (p->rows + wave - 1) / wave);
+    unit = (int)run_length(p->rows, p->seqs, 148 * ctas, 2 * groups);
     const int whole = batch * groups;      // whole batches, unless the rows are few
     if (unit >= whole) unit = (unit + whole - 1) / whole * whole;
     slots = slot_bound(p->rows, p->seqs, 1, unit);

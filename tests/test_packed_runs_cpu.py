@@ -15,6 +15,7 @@ SOURCE = """
 #include "packed_runs.cuh"
 extern "C" int rows(int begin, int len, int64_t piece, int unit, int *r) { return prism::run_rows(begin, len, piece, unit, r[0], r[1]); }
 extern "C" int count(int len, int unit) { return prism::run_count(len, unit); }
+extern "C" int64_t length(int64_t rows, int seqs, int ctas, int64_t least) { return prism::run_length(rows, seqs, ctas, least); }
 """
 
 
@@ -24,6 +25,8 @@ def lib(tmp_path_factory):
     subprocess.run(["g++", "-O1", "-fwrapv", "-x", "c++", "-shared", "-fPIC", "-I", str(CSRC), "-", "-o", str(out)], input=SOURCE.encode(),
                    check=True)
     so = ctypes.CDLL(str(out))
+    so.length.argtypes = [ctypes.c_int64, ctypes.c_int, ctypes.c_int, ctypes.c_int64]
+    so.length.restype = ctypes.c_int64
     so.rows.argtypes = [ctypes.c_int, ctypes.c_int, ctypes.c_int64, ctypes.c_int, ctypes.POINTER(ctypes.c_int)]
     return so
 
@@ -49,6 +52,19 @@ def test_runs_cover_a_sequence_exactly(lib, rows, seqs):
                 at = r1
             assert at == begin + length
             assert _run(lib, begin, length, n, unit) is None and _run(lib, begin, length, -1, unit) is None
+
+
+@pytest.mark.parametrize("ctas", [148, 296, 1184])
+@pytest.mark.parametrize("rows", [61440, LIMIT])
+def test_the_longest_sequence_is_shared_out(lib, rows, ctas):
+    """However many sequences there are, one of half the rows is cut into a third of the CTAs' number of runs at least,
+    and with few sequences there are no more runs than CTAs."""
+    for seqs in (1, 12, 37, 74, 147, 148, 150, 1000, 65534):
+        unit = lib.length(rows, seqs, ctas, 1)
+        assert lib.count(rows // 2, unit) >= ctas // 3
+        if seqs <= ctas // 4:
+            assert rows // unit + seqs <= ctas + 1
+    assert lib.length(10, 1, ctas, 16) == 16
 
 
 def test_no_runs_without_rows(lib):
