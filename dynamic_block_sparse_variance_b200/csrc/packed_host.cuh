@@ -400,10 +400,13 @@ static int launch_norm_bwd_v(const NormBwdShape &s, const BlockNormArgs &a, cuda
   PRISM_TRACED("block_norm_bwd_kernel", st, launch_behind(kernel, dim3((unsigned)s.slots), s.threads, s.smem, st, a));
   return PRISM_OK;
 }
+// Two vectors a thread need 156 to 168 registers, which 384 threads (6144 channels) leave
+// each of them; beyond, the form of 512 threads has 128 and spills (6144 channels, bf16,
+// 7500 rows: 150 us against 205 with that form).
 template <typename TX, typename TY>
 static int launch_norm_bwd(const NormBwdShape &s, const BlockNormArgs &a, cudaStream_t st) {
   return s.V == 1 ? launch_norm_bwd_v<TX, TY, 1, 512>(s, a, st)
-                  : s.threads <= 320 ? launch_norm_bwd_v<TX, TY, 2, 320>(s, a, st) : launch_norm_bwd_v<TX, TY, 2, 512>(s, a, st);
+                  : s.threads <= 384 ? launch_norm_bwd_v<TX, TY, 2, 384>(s, a, st) : launch_norm_bwd_v<TX, TY, 2, 512>(s, a, st);
 }
 
 }  // namespace prism
