@@ -26,8 +26,8 @@
 // (a product's operands have one type); everything else is fp32.  A row of dS sums
 // to zero, so dQ has nothing of what the keys have in common; a row of rounded dS
 // does not, and dQ would take its sum times that common part, which in keys with a
-// bias is many times the rest (13 times: dQ off by 2% of its norm, and by 17% with
-// values like that).  The queries kind therefore sums each row of the dS that enter
+// bias is many times the rest (13 times, 1024 causal tokens: dQ off by 2.7% of its norm,
+// where 0.24% is what the roundings explain).  The queries kind therefore sums each row of the dS that enter
 // the product and takes the sum times the keys' common part (common_key) away at the
 // end: right for any vector in its place, since the true sum is zero.  It is not where
 // o and lse belong to a softmax over more keys than this call's (shares of the keys

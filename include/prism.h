@@ -360,7 +360,7 @@ int prism_packed_workspace_size(const prism_packed_params *p, int kind, size_t *
 /*
  * Forward: O_r = softmax(scale q_r K^T) V over the keys that row r sees, and
  * LSE_r, the natural log of the sum of their exponentials.  A row that sees no
- * key gets O = 0 and LSE = -inf.
+ * key gets O = 0 and LSE = -inf; one that sees a NaN gets NaN.
  *   q, k, v        bf16, 16-byte aligned
  *   q_off, k_off   [seqs + 1] row offsets, nullable (an even split)
  *   k_used         [seqs] int32, nullable: only the first k_used[b] rows of
@@ -384,7 +384,8 @@ int prism_packed_attn_fwd(const prism_packed_params *p, const void *q, const voi
  * Backward of prism_packed_attn_fwd: dq, dk, dv (bf16) from dout (bf16), o, lse
  * and, nullable, o_res.  dk and dv sum over the query heads of a group; key
  * rows that no query sees, and rows behind k_used, get zero.  Results do
- * not change from run to run.  o and lse may belong to a softmax over more keys
+ * not change from run to run.  All of q, k, v and dout within a sequence has to be
+ * finite here: what is masked meets a zero in the products.  o and lse may belong to a softmax over more keys
  * than the call's (shares of the keys joined by their LSE): the gradients are then
  * the call's part.
  */
