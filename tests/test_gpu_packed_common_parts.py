@@ -54,7 +54,8 @@ def test_an_average_of_equal_values_is_that_value(lq, lk, heads, kv, dim):
 @pytest.mark.parametrize("causal", [True, False])
 @pytest.mark.parametrize("dim", [64, 128])
 @pytest.mark.parametrize("k_common,v_common", [(0.0, 13.0), (13.0, 0.0), (13.0, 13.0)])
-@pytest.mark.parametrize("lq,lk,heads,kv", [([600], [600], 2, 2), ([300, 37, 500], [300, 90, 500], 4, 2), ([60], [60], 6, 2)])
+@pytest.mark.parametrize("lq,lk,heads,kv", [([600], [600], 2, 2), ([300, 37, 500], [300, 90, 500], 4, 2), ([60], [60], 6, 2),
+                                           ([3, 2], [1000, 770], 4, 2), ([9], [2000], 8, 2)])
 def test_gradients_beside_common_parts(lq, lk, heads, kv, k_common, v_common, dim, causal):
     """A row of dS = P (dP - D) sums to zero, so dQ = scale dS K has nothing of the keys' common part, and D takes the
     values' out of dP. Three independent roundings (the operand dS, P inside D, the result), each of a mean square of
